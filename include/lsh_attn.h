@@ -308,6 +308,152 @@ lsh_status lsh_topk_forward(const lsh_topk_desc *desc, const void *x, const void
                             const void *proj, void *out, float *lse, int32_t *cand,
                             void *workspace, size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions with one to four axes, a paged cache of shared-QK rows and
+ * values, and attention of new tokens over it: what generating from a causal
+ * shared-QK model needs beside the forward pass. Positions inside the shared
+ * vectors and a cache have no counterpart on the pages; the attention keeps
+ * their rules (unit keys, 1/sqrt(d), a token sees itself only when alone).
+ *
+ * Conventions as above, and for the calls below
+ *   - Rows are given with three strides, in elements, for (batch, head,
+ *     position); the d values of a row are contiguous. Row pointers are
+ *     16-byte aligned and strides multiples of 16 bytes, so both
+ *     [B][H][n][d] and the projections' [B][n][H][d] are read in place.
+ *     Strides of inputs may be 0 (one row for all); written rows must not
+ *     overlap (LSH_ERR_INVALID_ARG). n rows per sequence are at most 2^20.
+ *   - Lengths, page numbers and positions are read on the device: a captured
+ *     graph may be replayed after they change.
+ *   - Nothing is allocated and no call synchronises.
+ */
+#define LSH_ROPE_MAX_AXES 4
+
+/* How a row's dimensions are rotated. Axis a turns the dims[a] dimensions
+ * after those of the axes before it, in dims[a] / 2 pairs; dimensions after
+ * the last axis are left as they are. */
+typedef struct {
+    int32_t axes;                    /* 1 .. 4 (lsh_cache_append: 0 = no rotation) */
+    int32_t dims[LSH_ROPE_MAX_AXES]; /* even, >= 2, sum <= d */
+    int32_t adjacent; /* pair i of an axis: its dimensions 2i and 2i + 1 (1),
+                       * or i and i + dims / 2 (0) */
+} lsh_rope_axes;
+
+typedef struct {
+    int32_t batch, heads, n, d;  /* d in {64, 128} */
+    int32_t dtype;               /* lsh_dtype of x and out */
+    int32_t inverse;             /* 1: rotate by the negative angles */
+    int32_t pos_batched;         /* positions [axes][batch][n] (1) or [axes][n] (0) */
+    lsh_rope_axes rot;
+    int64_t x_stride[3], out_stride[3];
+} lsh_rope_desc;
+
+/* Rotary positions: pair (lo, hi) of axis a, the p-th pair of all, turns by
+ * t = positions[a] * freqs[p]:
+ *   out[lo] = x[lo] cos t - x[hi] sin t,  out[hi] = x[lo] sin t + x[hi] cos t.
+ * The angle is formed in fp64 and reduced there, so far positions keep their
+ * precision; the rotation is fp32 and rounds once. inverse = 1 is the
+ * gradient with respect to x (and undoes the call). positions int32, any sign;
+ * freqs [sum dims / 2] fp32. out may be x itself with the same strides, else
+ * they must not overlap. */
+lsh_status lsh_rope(const lsh_rope_desc *desc, const void *x, const int32_t *positions,
+                    const float *freqs, void *out, void *stream);
+
+typedef enum { LSH_CACHE_BF16 = 0, LSH_CACHE_I8 = 1 } lsh_cache_format;
+
+/* A paged cache. A page holds page_size consecutive tokens of one sequence
+ * for every head. */
+typedef struct {
+    int32_t pages;      /* pages in the pool */
+    int32_t heads;
+    int32_t page_size;  /* 16, 32, 64 or 128 tokens */
+    int32_t d;          /* 64 or 128 */
+    int32_t format;     /* lsh_cache_format */
+} lsh_cache_desc;
+
+/* Its memory, 16-byte aligned, owned by the caller:
+ *   k   [pages][heads][page_size][d]           rows of x, bf16 or int8
+ *   v   [pages][heads][page_size / 16][d][16]  values, bf16 or int8: groups of
+ *       16 tokens, dimension-major inside (the order the attention's P V
+ *       product reads)
+ *   key_inv_norm [pages][heads][page_size]     fp32, 1/||x|| (0 below 2^-126)
+ *   k_scale, v_scale [pages][heads]            fp32, int8 only: a power of two
+ *       s for each page and head; a stored q stands for q * s
+ *   status  NULL, or at least 256 bytes, zeroed by the caller: the kernels
+ *       record the first error they meet (LSH_ERR_DEVICE) and leave it until
+ *       the caller clears it; lsh_attn_get_device_status reads it. */
+typedef struct {
+    void *k, *v;
+    float *key_inv_norm, *k_scale, *v_scale;
+    void *status;
+} lsh_cache;
+
+/* Rows that a call appends, reads back or attends from. */
+typedef struct {
+    int32_t batch;      /* sequences, at most 65535 */
+    int32_t n;          /* rows of each (padded batch: the most) */
+    int32_t max_pages;  /* columns of page_table */
+    int32_t pos_batched;              /* lsh_cache_append: as in lsh_rope_desc */
+    int64_t x_stride[3], v_stride[3]; /* x / out and v (lsh_cache_attend: x only) */
+    int64_t out_stride[3];            /* xr, or the attention's out */
+} lsh_cache_rows;
+
+/* Tables of the calls below, int32 on the device: page_table
+ * [batch][max_pages], the page of each page_size tokens of a sequence (only
+ * the entries of tokens that are read or written count); seq_len [batch], the
+ * tokens that a sequence holds before the call's n rows; n_valid [batch], how
+ * many of the n rows each sequence has (NULL: all n). A sequence with
+ * seq_len < 0, n_valid outside [0, n] or more tokens than max_pages pages
+ * hold is taken to have no rows, and a page number outside [0, pages) to hold
+ * nothing: neither is read or written, and both are recorded in the status. */
+
+/* Append rows seq_len .. seq_len + n_valid - 1 of every sequence: x, rotated
+ * by `rot` (as lsh_rope, result rounded to bf16; rot->axes 0 or rot NULL: as
+ * it is), and v, both bf16; 1/||x|| is taken of the row as it is given. xr,
+ * unless NULL, receives the rotated rows (the queries of lsh_cache_attend),
+ * zeros past n_valid. Slots of other tokens are left as they are.
+ * int8: a page's scale is the smallest power of two s >= 2^-126 such that
+ * 127 s covers its rows' finite values; a row that raises it has the earlier
+ * rows of the page rounded again from what is stored, q' = rint(q s / s').
+ * The first row of a page sets its scale afresh. Infinities are stored as
+ * +-127 s, NaN as 0, and recorded in the status.
+ * A page that is written must belong to one sequence of the call and stand in
+ * its table once; a prefix that several sequences share may be read by all. */
+lsh_status lsh_cache_append(const lsh_cache_desc *desc, const lsh_cache *cache,
+                            const lsh_cache_rows *rows, const lsh_rope_axes *rot, const void *x,
+                            const void *v, const int32_t *positions, const float *freqs,
+                            const int32_t *page_table, const int32_t *seq_len,
+                            const int32_t *n_valid, void *xr, void *stream);
+
+/* Read rows start .. start + n_valid - 1 of every sequence back as values:
+ * x (rotated as they were stored) and v, bf16 with x_stride and v_stride;
+ * rows past n_valid, and those of bad pages, are zeros. `start` takes the
+ * place of seq_len. For lsh_attn_forward over cached tokens, among others. */
+lsh_status lsh_cache_gather(const lsh_cache_desc *desc, const lsh_cache *cache,
+                            const lsh_cache_rows *rows, const int32_t *page_table,
+                            const int32_t *start, const int32_t *n_valid, void *x, void *v,
+                            void *stream);
+
+/* Workspace bytes of lsh_cache_attend (256-byte aligned; contents need not be
+ * kept or cleared between calls). */
+lsh_status lsh_cache_attend_workspace_size(const lsh_cache_desc *desc,
+                                           const lsh_cache_rows *rows, size_t *bytes);
+
+/* Attention of the n newest tokens of every sequence, whose rows
+ * lsh_cache_append has stored: token t (0 .. n_valid - 1) at position
+ * p = seq_len + t sees every cached token j <= p with the logit
+ *   x_t . k_j key_inv_norm_j / sqrt(d),   and -1e5 for itself (j = p),
+ * as lsh_attn_dense_forward does with causal = 1; x are the (rotated) rows in
+ * bf16, k_j and v_j the cache's values.
+ *   out bf16 (out_stride), lse [batch][heads][n] fp32, natural log.
+ * Rows past n_valid, and rows that see nothing (bad pages), are zeros with
+ * lse = -inf. Made for few tokens a sequence (one, or a handful of drafted
+ * ones): every eight rows read the cache once. Deterministic on one device. */
+lsh_status lsh_cache_attend(const lsh_cache_desc *desc, const lsh_cache *cache,
+                            const lsh_cache_rows *rows, const void *x,
+                            const int32_t *page_table, const int32_t *seq_len,
+                            const int32_t *n_valid, void *out, float *lse, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
 /* Static, human-readable name of a status code. */
 const char *lsh_attn_status_string(lsh_status status);
 

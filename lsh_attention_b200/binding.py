@@ -8,6 +8,7 @@ library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -28,7 +29,9 @@ EXPORTS = ("lsh_attn_workspace_size", "lsh_attn_hash", "lsh_attn_sort", "lsh_att
            "lsh_attn_sort_noalloc", "lsh_attn_selftest_wait_timeout",
            "lsh_attn_dense_workspace_size", "lsh_attn_dense_forward",
            "lsh_attn_backward_workspace_size", "lsh_attn_backward", "lsh_rev_workspace_size",
-           "lsh_rev_block", "lsh_topk_workspace_size", "lsh_topk_forward",
+           "lsh_rev_block", "lsh_topk_workspace_size", "lsh_topk_forward", "lsh_rope",
+           "lsh_cache_append", "lsh_cache_gather", "lsh_cache_attend_workspace_size",
+           "lsh_cache_attend",
            "lsh_attn_status_string")
 
 
@@ -55,6 +58,36 @@ class LshRevWeights(ctypes.Structure):
 class LshTopkDesc(ctypes.Structure):
     _fields_ = [(k, ctypes.c_int32) for k in
                 ("batch", "heads", "n", "d", "n_buckets", "n_bits", "top_k", "rounds", "causal")]
+
+
+LSH_CACHE_BF16, LSH_CACHE_I8 = 0, 1
+ROPE_MAX_AXES = 4  # LSH_ROPE_MAX_AXES
+
+
+class LshRopeAxes(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("dims", ctypes.c_int32 * ROPE_MAX_AXES),
+                ("adjacent", ctypes.c_int32)]
+
+
+class LshRopeDesc(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int32) for k in
+                 ("batch", "heads", "n", "d", "dtype", "inverse", "pos_batched")] +
+                [("rot", LshRopeAxes), ("x_stride", ctypes.c_int64 * 3),
+                 ("out_stride", ctypes.c_int64 * 3)])
+
+
+class LshCacheDesc(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_int32) for k in ("pages", "heads", "page_size", "d", "format")]
+
+
+class LshCacheMemory(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in
+                ("k", "v", "key_inv_norm", "k_scale", "v_scale", "status")]
+
+
+class LshCacheRows(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_int32) for k in ("batch", "n", "max_pages", "pos_batched")] +
+                [(k, ctypes.c_int64 * 3) for k in ("x_stride", "v_stride", "out_stride")])
 
 
 class LshAttnError(RuntimeError):
@@ -105,6 +138,12 @@ def load() -> ctypes.CDLL:
                                                     ctypes.POINTER(sz)]
             lib.lsh_topk_forward.argtypes = [ctypes.POINTER(LshTopkDesc), vp, vp, vp, vp, vp, vp,
                                              vp, sz, vp]
+            lib.lsh_rope.argtypes = [ctypes.POINTER(LshRopeDesc), vp, vp, vp, vp, vp]
+            cp, mp, rp = (ctypes.POINTER(t) for t in (LshCacheDesc, LshCacheMemory, LshCacheRows))
+            lib.lsh_cache_append.argtypes = [cp, mp, rp, ctypes.POINTER(LshRopeAxes)] + [vp] * 9
+            lib.lsh_cache_gather.argtypes = [cp, mp, rp] + [vp] * 6
+            lib.lsh_cache_attend_workspace_size.argtypes = [cp, rp, ctypes.POINTER(sz)]
+            lib.lsh_cache_attend.argtypes = [cp, mp, rp] + [vp] * 7 + [sz, vp]
             lib.lsh_attn_status_string.argtypes = [ctypes.c_int]
             lib.lsh_attn_status_string.restype = ctypes.c_char_p
             for f in EXPORTS[:-1]:
@@ -407,6 +446,266 @@ def lsh_topk_forward(x, v, proj, *, n_buckets: int, top_k: int, causal: bool,
     _check(load().lsh_topk_forward(ctypes.byref(desc), _ptr(x), _ptr(v), _ptr(proj), _ptr(out),
                                    _ptr(lse), _ptr(cand), _ptr(ws), ws.numel(), _stream(stream)))
     return (out, lse, cand) if return_candidates else (out, lse)
+
+
+def _rows_strides(t, name: str, dtype, shape) -> tuple:
+    """(batch, head, position) strides of rows [B, H, n, d] whose d values are contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # an axis of one entry is never stepped along; torch gives it any stride
+    return (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
+
+
+@functools.lru_cache(maxsize=None)
+def _axes(axis_dims: tuple, adjacent: bool) -> LshRopeAxes:
+    return LshRopeAxes(len(axis_dims), (ctypes.c_int32 * ROPE_MAX_AXES)(*axis_dims),
+                       int(adjacent))
+
+
+def _check_angles(positions, freqs, axis_dims: tuple, B: int, n: int) -> bool:
+    """Check positions [axes, B, n] or [axes, n] and freqs; whether positions have a batch axis."""
+    if len(axis_dims) > ROPE_MAX_AXES:
+        raise ValueError(f"axis_dims: at most {ROPE_MAX_AXES} axes, got {len(axis_dims)}")
+    batched = positions.dim() == 3
+    _require(positions, "positions", torch.int32,
+             (len(axis_dims), B, n) if batched else (len(axis_dims), n))
+    _require(freqs, "freqs", torch.float32, (sum(a // 2 for a in axis_dims),))
+    return batched
+
+
+@functools.lru_cache(maxsize=1024)
+def _rope_desc(B, H, n, d, dtype, inverse, batched, axis_dims, adjacent, xs, os_) -> LshRopeDesc:
+    return LshRopeDesc(B, H, n, d, dtype, inverse, batched, _axes(axis_dims, adjacent),
+                       (ctypes.c_int64 * 3)(*xs), (ctypes.c_int64 * 3)(*os_))
+
+
+@functools.lru_cache(maxsize=1024)
+def _cache_rows(B, n, max_pages, batched, xs, vs=(0, 0, 0), os_=(0, 0, 0)) -> LshCacheRows:
+    three = ctypes.c_int64 * 3
+    return LshCacheRows(B, n, max_pages, batched, three(*xs), three(*vs), three(*os_))
+
+
+def _on_stream(stream, call, *tensors):
+    """Run call() with `stream` current, its results made in that stream's memory; the tensors
+    are not handed out again before the stream has passed."""
+    with torch.cuda.stream(stream):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return call()
+
+
+def lsh_rope(x, positions, freqs, *, axis_dims, adjacent: bool = False, inverse: bool = False,
+             out=None, stream=None):
+    """Rotary positions on the rows of x [B, H, n, d] (fp32 or bf16; any strides with the last
+    dimension contiguous). Axis a turns axis_dims[a] dimensions by positions[a] * freqs;
+    positions int32 [axes, B, n] or [axes, n], freqs fp32 [sum(axis_dims) / 2] (one frequency
+    for each pair). `adjacent`: pairs are neighbouring dimensions, else the halves of an axis.
+    `inverse` turns back, which is the gradient with respect to x. Returns out [B, H, n, d];
+    out may be x itself."""
+    _on_current_device(stream, x=x, positions=positions, freqs=freqs, out=out)
+    if stream is not None:
+        return _on_stream(stream, lambda: lsh_rope(x, positions, freqs, axis_dims=axis_dims,
+                                                   adjacent=adjacent, inverse=inverse, out=out),
+                          x, positions, freqs, out)
+    B, H, n, d = x.shape
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {x.dtype}")
+    axis_dims = tuple(axis_dims)
+    xs = _rows_strides(x, "x", x.dtype, (B, H, n, d))
+    batched = _check_angles(positions, freqs, axis_dims, B, n)
+    if out is None:
+        out = torch.empty((B, H, n, d), dtype=x.dtype, device=x.device)
+    desc = _rope_desc(B, H, n, d, _DTYPES[x.dtype], int(inverse), batched, axis_dims, adjacent,
+                      xs, _rows_strides(out, "out", x.dtype, (B, H, n, d)))
+    _check(load().lsh_rope(ctypes.byref(desc), x.data_ptr(), positions.data_ptr(),
+                           freqs.data_ptr(), out.data_ptr(), _stream(None)))
+    return out
+
+
+class LshCache:
+    """A paged cache of rows of x and v for every head, bf16 or int8 (see lsh_cache in
+    lsh_attn.h for the layouts):
+
+    k [pages, heads, page_size, d], v [pages, heads, page_size / 16, d, 16],
+    key_inv_norm [pages, heads, page_size] fp32, and for int8 k_scale and v_scale
+    [pages, heads] fp32. status: int32 [64], zeroed here; the calls record the first error they
+    meet on the device there. `LshCache.empty` makes one."""
+
+    def __init__(self, k, v, key_inv_norm, k_scale=None, v_scale=None, status=None):
+        pages, heads, page, d = k.shape
+        if k.dtype not in (torch.bfloat16, torch.int8):
+            raise TypeError(f"k must be torch.bfloat16 or torch.int8, got {k.dtype}")
+        self.int8 = k.dtype == torch.int8
+        _require(k, "k", None, None)
+        _require(v, "v", k.dtype, (pages, heads, page // 16, d, 16))
+        _require(key_inv_norm, "key_inv_norm", torch.float32, (pages, heads, page))
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if self.int8 != (t is not None):
+                raise ValueError(f"{name} belongs to an int8 cache, and to no other")
+            if t is not None:
+                _require(t, name, torch.float32, (pages, heads))
+        if status is None:
+            status = torch.zeros(64, dtype=torch.int32, device=k.device)
+        _require(status, "status", torch.int32, (64,))
+        self.k, self.v, self.key_inv_norm = k, v, key_inv_norm
+        self.k_scale, self.v_scale, self.status = k_scale, v_scale, status
+        self.tensors = {"k": k, "v": v, "key_inv_norm": key_inv_norm, "k_scale": k_scale,
+                        "v_scale": v_scale, "status": status}
+        if any(t is not None and t.device != k.device for t in self.tensors.values()):
+            raise ValueError("all of a cache lies on one device")
+        self.pages, self.heads, self.page_size, self.d = pages, heads, page, d
+        self.desc = LshCacheDesc(pages, heads, page, d,
+                                 LSH_CACHE_I8 if self.int8 else LSH_CACHE_BF16)
+        self.memory = LshCacheMemory(*[None if t is None else t.data_ptr()
+                                       for t in self.tensors.values()])
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, page_size: int, d: int, *, int8: bool = False,
+              device="cuda") -> "LshCache":
+        """A cache whose pages hold nothing yet."""
+        dt = torch.int8 if int8 else torch.bfloat16
+        scales = [torch.empty((pages, heads), dtype=torch.float32, device=device)
+                  for _ in range(2)] if int8 else []
+        return cls(torch.empty((pages, heads, page_size, d), dtype=dt, device=device),
+                   torch.empty((pages, heads, page_size // 16, d, 16), dtype=dt, device=device),
+                   torch.empty((pages, heads, page_size), dtype=torch.float32, device=device),
+                   *scales)
+
+    def get_device_status(self, stream=None) -> int:
+        """Synchronise and return the first error recorded since the status was cleared."""
+        return lsh_attn_get_device_status(self.status, stream)
+
+    def clear_status(self) -> None:
+        self.status.zero_()
+
+
+def _check_tables(cache, B: int, page_table, seq_len, n_valid, what: str = "seq_len") -> None:
+    _require(page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
+    _require(seq_len, what, torch.int32, (B,))
+    if n_valid is not None:
+        _require(n_valid, "n_valid", torch.int32, (B,))
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def lsh_cache_append(cache: LshCache, x, v, page_table, seq_len, *, n_valid=None, positions=None,
+                     freqs=None, axis_dims=(), adjacent: bool = False, xr=None, stream=None):
+    """Append the rows x, v [B, H, n, d] (bf16, any strides with the last dimension contiguous)
+    as tokens seq_len .. of every sequence, x rotated on the way if `axis_dims` is given (as
+    lsh_rope). page_table int32 [B, max_pages], seq_len int32 [B], n_valid int32 [B] or None
+    (all n rows). Returns the rotated rows [B, H, n, d] (zeros past n_valid), the queries of
+    lsh_cache_attend; without a rotation and without `xr`, x itself. xr may be x."""
+    _on_current_device(stream, x=x, v=v, page_table=page_table, seq_len=seq_len, n_valid=n_valid,
+                       positions=positions, freqs=freqs, xr=xr, cache=cache.k)
+    if stream is not None:
+        return _on_stream(
+            stream, lambda: lsh_cache_append(
+                cache, x, v, page_table, seq_len, n_valid=n_valid, positions=positions,
+                freqs=freqs, axis_dims=axis_dims, adjacent=adjacent, xr=xr),
+            x, v, page_table, seq_len, n_valid, positions, freqs, xr, *cache.tensors.values())
+    B, H, n, d = shape = tuple(x.shape)
+    if (H, d) != (cache.heads, cache.d):
+        raise ValueError(f"x has {H} heads of {d}, the cache {cache.heads} of {cache.d}")
+    xs = _rows_strides(x, "x", torch.bfloat16, shape)
+    vs = _rows_strides(v, "v", torch.bfloat16, shape)
+    _check_tables(cache, B, page_table, seq_len, n_valid)
+    axis_dims = tuple(axis_dims)
+    batched = False
+    if axis_dims:
+        if positions is None or freqs is None:
+            raise ValueError("a rotation needs positions and freqs")
+        batched = _check_angles(positions, freqs, axis_dims, B, n)
+        if xr is None:
+            xr = torch.empty(shape, dtype=x.dtype, device=x.device)
+    os_ = _rows_strides(xr, "xr", torch.bfloat16, shape) if xr is not None else (0, 0, 0)
+    rows = _cache_rows(B, n, page_table.shape[1], batched, xs, vs, os_)
+    _check(load().lsh_cache_append(
+        ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows),
+        ctypes.byref(_axes(axis_dims, adjacent)), x.data_ptr(), v.data_ptr(), _opt(positions),
+        _opt(freqs), page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), _opt(xr),
+        _stream(None)))
+    return x if xr is None else xr
+
+
+def lsh_cache_gather(cache: LshCache, page_table, start, n: int, *, n_valid=None, x=None, v=None,
+                     stream=None):
+    """Read n rows from position start[b] of every sequence back as values. start int32 [B],
+    n_valid int32 [B] or None. Returns x, v [B, H, n, d] bf16, zeros past n_valid."""
+    _on_current_device(stream, page_table=page_table, start=start, n_valid=n_valid, x=x, v=v,
+                       cache=cache.k)
+    if stream is not None:
+        return _on_stream(stream, lambda: lsh_cache_gather(cache, page_table, start, n,
+                                                           n_valid=n_valid, x=x, v=v),
+                          page_table, start, n_valid, x, v, *cache.tensors.values())
+    B = page_table.shape[0]
+    shape = (B, cache.heads, n, cache.d)
+    _check_tables(cache, B, page_table, start, n_valid, "start")
+    x, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None else t
+            for t in (x, v))
+    rows = _cache_rows(B, n, page_table.shape[1], False,
+                       _rows_strides(x, "x", torch.bfloat16, shape),
+                       _rows_strides(v, "v", torch.bfloat16, shape))
+    _check(load().lsh_cache_gather(
+        ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows),
+        page_table.data_ptr(), start.data_ptr(), _opt(n_valid), x.data_ptr(), v.data_ptr(),
+        _stream(None)))
+    return x, v
+
+
+def lsh_cache_attend(cache: LshCache, x, page_table, seq_len, *, n_valid=None, out=None, lse=None,
+                     ws=None, stream=None):
+    """Shared-QK attention of the n newest tokens of every sequence over the cache, after
+    lsh_cache_append has stored them: x [B, H, n, d] bf16, the rotated rows that it returned,
+    with its page_table, seq_len (before those tokens) and n_valid. Returns out [B, H, n, d]
+    bf16 and lse [B, H, n] fp32; rows past n_valid are zeros and -inf."""
+    _on_current_device(stream, x=x, page_table=page_table, seq_len=seq_len, n_valid=n_valid,
+                       out=out, lse=lse, ws=ws, cache=cache.k)
+    if stream is not None:
+        return _on_stream(stream, lambda: lsh_cache_attend(cache, x, page_table, seq_len,
+                                                           n_valid=n_valid, out=out, lse=lse,
+                                                           ws=ws),
+                          x, page_table, seq_len, n_valid, out, lse, ws, *cache.tensors.values())
+    B, H, n, d = shape = tuple(x.shape)
+    if (H, d) != (cache.heads, cache.d):
+        raise ValueError(f"x has {H} heads of {d}, the cache {cache.heads} of {cache.d}")
+    xs = _rows_strides(x, "x", torch.bfloat16, shape)
+    _check_tables(cache, B, page_table, seq_len, n_valid)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    if lse is None:
+        lse = torch.empty((B, H, n), dtype=torch.float32, device=x.device)
+    else:
+        _require(lse, "lse", torch.float32, (B, H, n))
+    rows = _cache_rows(B, n, page_table.shape[1], False, xs, (0, 0, 0),
+                       _rows_strides(out, "out", torch.bfloat16, shape))
+    need = _attend_workspace(B, n, H, d, cache.page_size, cache.int8)
+    if ws is None:
+        # a graph under capture keeps its own: the cached one may grow and go away
+        ws = (torch.empty(need, dtype=torch.uint8, device=x.device)
+              if torch.cuda.is_current_stream_capturing() else _scratch(x.device, None, need))
+    _check(load().lsh_cache_attend(
+        ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows), x.data_ptr(),
+        page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), out.data_ptr(), lse.data_ptr(),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(None)))
+    return out, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def _attend_workspace(B: int, n: int, heads: int, d: int, page_size: int, int8: bool) -> int:
+    desc = LshCacheDesc(1, heads, page_size, d, LSH_CACHE_I8 if int8 else LSH_CACHE_BF16)
+    out = ctypes.c_size_t(0)
+    _check(load().lsh_cache_attend_workspace_size(
+        ctypes.byref(desc), ctypes.byref(_cache_rows(B, n, 1, False, (0, 0, 0))),
+        ctypes.byref(out)))
+    return out.value
 
 
 def _scratch(device, stream, need: int) -> torch.Tensor:

@@ -37,7 +37,7 @@ def build(force: bool = False, ptxas_verbose: bool = False) -> str:
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [NVCC] + FLAGS + (["-Xptxas", "-v"] if ptxas_verbose else []) + \
         ["-o", tmp] + [os.path.join(CSRC, f) for f in ("lsh_attn.cu", "lsh_attn_noalloc.cu",
-                                                        "lsh_rev.cu")]
+                                                        "lsh_rev.cu", "lsh_cache.cu")]
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
     return LIB

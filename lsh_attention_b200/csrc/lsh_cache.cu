@@ -1,0 +1,310 @@
+// Host side of the rotary and cache entry points declared in
+// include/lsh_attn.h: argument checks and launches on the caller's stream.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "cache_attend.cuh"
+#include "lsh_attn.h"
+#include "rope.cuh"
+#include "tma_host.cuh"
+
+namespace {
+
+using namespace lsh;
+
+inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+inline lsh_status last_cuda() {
+  return cudaGetLastError() == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+}
+
+// Rows [B][H][n] of d contiguous elements: strides non-negative multiples of
+// 16 bytes, small enough that no byte offset leaves 63 bits.
+bool strides_ok(const int64_t (&s)[3], int esize) {
+  for (int64_t v : s)
+    if (v < 0 || v * esize % 16 != 0 || v >= (int64_t(1) << 44)) return false;
+  return true;
+}
+
+// Whether rows that are written lie apart: sorted by stride, every axis steps
+// over what the axes inside it span.
+bool rows_apart(const int64_t (&s)[3], int B, int H, int n, int d) {
+  std::pair<int64_t, int64_t> ax[3] = {{s[0], B}, {s[1], H}, {s[2], n}};
+  std::sort(ax, ax + 3);
+  int64_t span = d;  // elements from the first to one past the last so far
+  for (const auto& a : ax) {
+    if (a.second == 1) continue;
+    if (a.first < span) return false;
+    span += a.first * (a.second - 1);
+  }
+  return true;
+}
+
+constexpr int kMaxRows = 1 << 20;
+
+// Checks `rot` and fills the plan. 0: no rotation is asked for.
+lsh_status check_rot(const lsh_rope_axes* rot, int d, RotPlan* R) {
+  *R = RotPlan{};
+  if (!rot || rot->axes == 0) return LSH_OK;
+  if (rot->axes < 0 || rot->axes > LSH_ROPE_MAX_AXES || (rot->adjacent != 0 && rot->adjacent != 1))
+    return LSH_ERR_INVALID_ARG;
+  int at = 0;
+  for (int a = 0; a < rot->axes; ++a) {
+    if (rot->dims[a] < 2 || rot->dims[a] % 2 != 0 || rot->dims[a] > d - at)
+      return LSH_ERR_INVALID_ARG;
+    R->off[a] = at;
+    R->half[a] = rot->dims[a] / 2;
+    at += rot->dims[a];
+  }
+  R->axes = rot->axes;
+  R->adjacent = rot->adjacent;
+  R->pairs = at / 2;
+  return LSH_OK;
+}
+
+// Pairs a thread turns together: a run of them fills at most 16 bytes. Adjacent
+// pairs always do. Pairs of halves lie in two runs that have to stay inside
+// their axis, so the width divides every axis's pairs (24 dimensions: 12 pairs,
+// runs of 4, 8 bytes).
+int rot_width(const RotPlan& R, int esize) {
+  int w = 16 / esize;
+  if (!R.adjacent)
+    for (int a = 0; a < R.axes; ++a)
+      while (R.half[a] % w != 0) w /= 2;
+  return w;
+}
+
+template <typename T, int W>
+lsh_status launch_rope_w(const RopeArgs& A, const void* x, void* out, cudaStream_t st) {
+  const int64_t threads = (int64_t)A.n * (A.d / (2 * W));
+  const int64_t blocks = (threads + 255) / 256;
+  const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>((int64_t)A.B * A.head_groups, 65535));
+  auto kern = k_rope<T, W, false>;
+  if constexpr (W * sizeof(T) == 16)  // adjacent pairs always come by 16 bytes
+    if (A.rot.adjacent) kern = k_rope<T, W, true>;
+  kern<<<grid, 256, 0, st>>>(static_cast<const T*>(x), static_cast<T*>(out), A);
+  return last_cuda();
+}
+
+// ---------------------------------------------------------------- cache calls
+lsh_status check_cache(const lsh_cache_desc* c, const lsh_cache* m, const lsh_cache_rows* r,
+                       const int32_t* table, const int32_t* len, const int32_t* valid,
+                       CacheView* C, SeqTables* S) {
+  if (!c || !r) return LSH_ERR_INVALID_ARG;
+  if (c->pages < 1 || c->heads < 1 || c->page_size < 1 || c->d < 1 ||
+      (c->format != LSH_CACHE_BF16 && c->format != LSH_CACHE_I8) || r->batch < 1 || r->n < 1 ||
+      r->max_pages < 1)
+    return LSH_ERR_INVALID_ARG;
+  if ((c->d != 64 && c->d != 128) || (c->page_size != 16 && c->page_size != 32 &&
+                                      c->page_size != 64 && c->page_size != 128))
+    return LSH_ERR_UNSUPPORTED;
+  if (r->batch > 65535 || c->heads > 65535 || r->n > kMaxRows) return LSH_ERR_UNSUPPORTED;
+  if (!m) return LSH_OK;  // sizes only
+  if (!m->k || !m->v || !m->key_inv_norm || !table || !len) return LSH_ERR_INVALID_ARG;
+  if (c->format == LSH_CACHE_I8 && (!m->k_scale || !m->v_scale)) return LSH_ERR_INVALID_ARG;
+  if (!aligned16(m->k) || !aligned16(m->v) || !aligned16(m->key_inv_norm) ||
+      !aligned16(m->status))
+    return LSH_ERR_INVALID_ARG;
+  *C = CacheView{m->k,        m->v,          m->key_inv_norm,
+                 m->k_scale,  m->v_scale,    static_cast<WsHeader*>(m->status),
+                 c->pages,    c->heads,      c->page_size, c->d};
+  *S = SeqTables{table, len, valid, r->batch, r->n, r->max_pages};
+  return LSH_OK;
+}
+
+template <int D, bool I8, int W, bool ADJ>
+lsh_status launch_append_w(const AppendArgs& A, cudaStream_t st) {
+  const size_t smem = append_smem(A.rows, D, A.rot.pairs);
+  auto kern = k_cache_append<D, I8, W, ADJ>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return LSH_ERR_CUDA;
+  const dim3 grid((unsigned)((A.S.n + A.rows - 2) / A.rows + 1),
+                  (unsigned)((A.C.H + A.heads_per - 1) / A.heads_per), (unsigned)A.S.B);
+  kern<<<grid, 256, smem, st>>>(A);
+  return last_cuda();
+}
+
+template <int D, bool I8>
+lsh_status launch_append(const AppendArgs& A, cudaStream_t st) {
+  if (A.rot.axes == 0) return launch_append_w<D, I8, 0, false>(A, st);
+  if (A.rot.adjacent) return launch_append_w<D, I8, 8, true>(A, st);
+  switch (rot_width(A.rot, 2)) {
+    case 8: return launch_append_w<D, I8, 8, false>(A, st);
+    case 4: return launch_append_w<D, I8, 4, false>(A, st);
+    case 2: return launch_append_w<D, I8, 2, false>(A, st);
+    default: return launch_append_w<D, I8, 1, false>(A, st);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+lsh_status lsh_rope(const lsh_rope_desc* desc, const void* x, const int32_t* positions,
+                    const float* freqs, void* out, void* stream) {
+  if (!desc) return LSH_ERR_INVALID_ARG;
+  const lsh_rope_desc& q = *desc;
+  if (q.batch < 1 || q.heads < 1 || q.n < 1 || q.d < 1 || (q.inverse != 0 && q.inverse != 1) ||
+      (q.pos_batched != 0 && q.pos_batched != 1) ||
+      (q.dtype != LSH_F32 && q.dtype != LSH_BF16) || q.rot.axes < 1)
+    return LSH_ERR_INVALID_ARG;
+  if (q.d != 64 && q.d != 128) return LSH_ERR_UNSUPPORTED;
+  RopeArgs A;
+  lsh_status s = check_rot(&q.rot, q.d, &A.rot);
+  if (s != LSH_OK) return s;
+  if (!x || !positions || !freqs || !out || !aligned16(x) || !aligned16(out))
+    return LSH_ERR_INVALID_ARG;
+  const int esize = q.dtype == LSH_BF16 ? 2 : 4;
+  if (!strides_ok(q.x_stride, esize) || !strides_ok(q.out_stride, esize) ||
+      !rows_apart(q.out_stride, q.batch, q.heads, q.n, q.d))
+    return LSH_ERR_INVALID_ARG;
+  A.pos = positions;
+  A.freqs = freqs;
+  A.B = q.batch;
+  A.H = q.heads;
+  A.n = q.n;
+  A.d = q.d;
+  A.pos_axis = q.pos_batched ? (int64_t)q.batch * q.n : q.n;
+  A.pos_batch = q.pos_batched ? q.n : 0;
+  for (int i = 0; i < 3; ++i) {
+    A.xs[i] = q.x_stride[i];
+    A.os[i] = q.out_stride[i];
+  }
+  A.sign = q.inverse ? -1.f : 1.f;
+  const int w = rot_width(A.rot, esize);
+  // heads are split over blocks until the card is filled
+  const int64_t blocks = ((int64_t)q.n * (q.d / (2 * w)) + 255) / 256 * q.batch;
+  const int64_t want = 8 * sm_count();
+  int groups = (int)std::min<int64_t>(q.heads, std::max<int64_t>(1, want / std::max<int64_t>(blocks, 1)));
+  A.heads_per = (q.heads + groups - 1) / groups;
+  A.head_groups = (q.heads + A.heads_per - 1) / A.heads_per;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (q.dtype == LSH_BF16) {
+    switch (w) {
+      case 8: return launch_rope_w<__nv_bfloat16, 8>(A, x, out, st);
+      case 4: return launch_rope_w<__nv_bfloat16, 4>(A, x, out, st);
+      case 2: return launch_rope_w<__nv_bfloat16, 2>(A, x, out, st);
+      default: return launch_rope_w<__nv_bfloat16, 1>(A, x, out, st);
+    }
+  }
+  switch (w) {
+    case 4: return launch_rope_w<float, 4>(A, x, out, st);
+    case 2: return launch_rope_w<float, 2>(A, x, out, st);
+    default: return launch_rope_w<float, 1>(A, x, out, st);
+  }
+}
+
+lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
+                            const lsh_cache_rows* rows, const lsh_rope_axes* rot, const void* x,
+                            const void* v, const int32_t* positions, const float* freqs,
+                            const int32_t* page_table, const int32_t* seq_len,
+                            const int32_t* n_valid, void* xr, void* stream) {
+  if (!cache) return LSH_ERR_INVALID_ARG;
+  AppendArgs A;
+  lsh_status s = check_cache(desc, cache, rows, page_table, seq_len, n_valid, &A.C, &A.S);
+  if (s != LSH_OK) return s;
+  if ((s = check_rot(rot, A.C.d, &A.rot)) != LSH_OK) return s;
+  if (!x || !v || !aligned16(x) || !aligned16(v) || !aligned16(xr)) return LSH_ERR_INVALID_ARG;
+  if (A.rot.axes > 0 && (!positions || !freqs)) return LSH_ERR_INVALID_ARG;
+  if (rows->pos_batched != 0 && rows->pos_batched != 1) return LSH_ERR_INVALID_ARG;
+  if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->v_stride, 2) ||
+      (xr && (!strides_ok(rows->out_stride, 2) ||
+              !rows_apart(rows->out_stride, A.S.B, A.C.H, A.S.n, A.C.d))))
+    return LSH_ERR_INVALID_ARG;
+  A.x = static_cast<const __nv_bfloat16*>(x);
+  A.v = static_cast<const __nv_bfloat16*>(v);
+  A.xr = static_cast<__nv_bfloat16*>(xr);
+  A.pos = positions;
+  A.freqs = freqs;
+  A.pos_axis = rows->pos_batched ? (int64_t)A.S.B * A.S.n : A.S.n;
+  A.pos_batch = rows->pos_batched ? A.S.n : 0;
+  for (int i = 0; i < 3; ++i) {
+    A.xs[i] = rows->x_stride[i];
+    A.vs[i] = rows->v_stride[i];
+    A.os[i] = rows->out_stride[i];
+  }
+  const bool i8 = desc->format == LSH_CACHE_I8;
+  A.rows = i8 ? A.C.P : 32;
+  const int64_t blocks = (int64_t)((A.S.n + A.rows - 2) / A.rows + 1) * A.S.B;
+  const int64_t want = 8 * sm_count();
+  const int groups = (int)std::min<int64_t>(A.C.H, std::max<int64_t>(1, want / blocks));
+  A.heads_per = (A.C.H + groups - 1) / groups;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (A.C.d == 64) return i8 ? launch_append<64, true>(A, st) : launch_append<64, false>(A, st);
+  return i8 ? launch_append<128, true>(A, st) : launch_append<128, false>(A, st);
+}
+
+lsh_status lsh_cache_gather(const lsh_cache_desc* desc, const lsh_cache* cache,
+                            const lsh_cache_rows* rows, const int32_t* page_table,
+                            const int32_t* start, const int32_t* n_valid, void* x, void* v,
+                            void* stream) {
+  if (!cache) return LSH_ERR_INVALID_ARG;
+  GatherArgs A;
+  lsh_status s = check_cache(desc, cache, rows, page_table, start, n_valid, &A.C, &A.S);
+  if (s != LSH_OK) return s;
+  if (!x || !v || !aligned16(x) || !aligned16(v)) return LSH_ERR_INVALID_ARG;
+  if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->v_stride, 2) ||
+      !rows_apart(rows->x_stride, A.S.B, A.C.H, A.S.n, A.C.d) ||
+      !rows_apart(rows->v_stride, A.S.B, A.C.H, A.S.n, A.C.d))
+    return LSH_ERR_INVALID_ARG;
+  A.x = static_cast<__nv_bfloat16*>(x);
+  A.v = static_cast<__nv_bfloat16*>(v);
+  for (int i = 0; i < 3; ++i) {
+    A.xs[i] = rows->x_stride[i];
+    A.vs[i] = rows->v_stride[i];
+  }
+  A.groups = (A.S.n + kGroup - 2) / kGroup + 1;
+  const dim3 grid((unsigned)((A.groups + 7) / 8), (unsigned)A.C.H, (unsigned)A.S.B);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool i8 = desc->format == LSH_CACHE_I8;
+  auto kern = A.C.d == 64 ? (i8 ? k_cache_gather<64, true> : k_cache_gather<64, false>)
+                          : (i8 ? k_cache_gather<128, true> : k_cache_gather<128, false>);
+  kern<<<grid, 256, 0, st>>>(A);
+  return last_cuda();
+}
+
+lsh_status lsh_cache_attend_workspace_size(const lsh_cache_desc* desc, const lsh_cache_rows* rows,
+                                           size_t* bytes) {
+  lsh_status s = check_cache(desc, nullptr, rows, nullptr, nullptr, nullptr, nullptr, nullptr);
+  if (s != LSH_OK) return s;
+  if (!bytes) return LSH_ERR_INVALID_ARG;
+  *bytes = 256;
+  return LSH_OK;
+}
+
+lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
+                            const lsh_cache_rows* rows, const void* x, const int32_t* page_table,
+                            const int32_t* seq_len, const int32_t* n_valid, void* out, float* lse,
+                            void* ws, size_t ws_bytes, void* stream) {
+  if (!cache) return LSH_ERR_INVALID_ARG;
+  AttendArgs A;
+  lsh_status s = check_cache(desc, cache, rows, page_table, seq_len, n_valid, &A.C, &A.S);
+  if (s != LSH_OK) return s;
+  if (!x || !out || !lse || !aligned16(x) || !aligned16(out)) return LSH_ERR_INVALID_ARG;
+  if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->out_stride, 2) ||
+      !rows_apart(rows->out_stride, A.S.B, A.C.H, A.S.n, A.C.d))
+    return LSH_ERR_INVALID_ARG;
+  size_t need = 0;
+  if ((s = lsh_cache_attend_workspace_size(desc, rows, &need)) != LSH_OK) return s;
+  if (!ws || ((uintptr_t)ws & 255) != 0 || ws_bytes < need) return LSH_ERR_WORKSPACE;
+  A.x = static_cast<const __nv_bfloat16*>(x);
+  A.out = static_cast<__nv_bfloat16*>(out);
+  A.lse = lse;
+  for (int i = 0; i < 3; ++i) {
+    A.xs[i] = rows->x_stride[i];
+    A.os[i] = rows->out_stride[i];
+  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)A.S.n, (unsigned)A.C.H, (unsigned)A.S.B);
+  const bool i8 = desc->format == LSH_CACHE_I8;
+  auto kern = A.C.d == 64 ? (i8 ? k_cache_attend<64, true> : k_cache_attend<64, false>)
+                          : (i8 ? k_cache_attend<128, true> : k_cache_attend<128, false>);
+  kern<<<grid, 128, 0, st>>>(A);
+  return last_cuda();
+}
+
+}  // extern "C"
