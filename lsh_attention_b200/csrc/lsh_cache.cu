@@ -140,6 +140,50 @@ lsh_status launch_append(const AppendArgs& A, cudaStream_t st) {
   }
 }
 
+// Workspace of the cached attention: for every block a record, and two partial
+// results of eight rows.
+struct AttendLayout {
+  int blocks;
+  size_t ml, part, total;
+};
+
+AttendLayout attend_layout(int d) {
+  AttendLayout L;
+  L.blocks = sm_count() * (d == 64 ? AttCfg<64, false>::kBlocks : AttCfg<128, false>::kBlocks);
+  const size_t rows = (size_t)L.blocks * 2 * kAttRows;
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  L.ml = up((size_t)L.blocks * 32);
+  L.part = L.ml + up(rows * 2 * sizeof(float));
+  L.total = L.part + up(rows * d * sizeof(float));
+  return L;
+}
+
+template <int D, bool I8>
+lsh_status launch_attend(const AttendArgs& A, cudaStream_t st) {
+  using Cfg = AttCfg<D, I8>;
+  static_assert(Cfg::kStages >= 3 && Cfg::kStages <= 8, "ring");
+  static_assert(sizeof(TileMeta) <= Cfg::kMeta, "stage header");
+  auto kern = k_cache_attend<D, I8>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
+      cudaSuccess)
+    return LSH_ERR_CUDA;
+  const unsigned blocks = (unsigned)attend_layout(D).blocks;
+  kern<<<blocks, kAttThreads, Cfg::kSmem, st>>>(A);
+  if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
+  // a table that holds one tile at most leaves nothing to join
+  if ((int64_t)A.S.max_pages * A.C.P <= kTileTok) return LSH_OK;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, (unsigned)std::min(A.S.n, kAttRows));
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_cache_combine<D>, A) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -272,7 +316,7 @@ lsh_status lsh_cache_attend_workspace_size(const lsh_cache_desc* desc, const lsh
   lsh_status s = check_cache(desc, nullptr, rows, nullptr, nullptr, nullptr, nullptr, nullptr);
   if (s != LSH_OK) return s;
   if (!bytes) return LSH_ERR_INVALID_ARG;
-  *bytes = 256;
+  *bytes = attend_layout(desc->d).total;
   return LSH_OK;
 }
 
@@ -288,9 +332,8 @@ lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
   if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->out_stride, 2) ||
       !rows_apart(rows->out_stride, A.S.B, A.C.H, A.S.n, A.C.d))
     return LSH_ERR_INVALID_ARG;
-  size_t need = 0;
-  if ((s = lsh_cache_attend_workspace_size(desc, rows, &need)) != LSH_OK) return s;
-  if (!ws || ((uintptr_t)ws & 255) != 0 || ws_bytes < need) return LSH_ERR_WORKSPACE;
+  const AttendLayout L = attend_layout(A.C.d);
+  if (!ws || ((uintptr_t)ws & 255) != 0 || ws_bytes < L.total) return LSH_ERR_WORKSPACE;
   A.x = static_cast<const __nv_bfloat16*>(x);
   A.out = static_cast<__nv_bfloat16*>(out);
   A.lse = lse;
@@ -298,13 +341,14 @@ lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
     A.xs[i] = rows->x_stride[i];
     A.os[i] = rows->out_stride[i];
   }
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  A.rec = reinterpret_cast<int*>(w);
+  A.part_ml = reinterpret_cast<float*>(w + L.ml);
+  A.part = reinterpret_cast<float*>(w + L.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)A.S.n, (unsigned)A.C.H, (unsigned)A.S.B);
   const bool i8 = desc->format == LSH_CACHE_I8;
-  auto kern = A.C.d == 64 ? (i8 ? k_cache_attend<64, true> : k_cache_attend<64, false>)
-                          : (i8 ? k_cache_attend<128, true> : k_cache_attend<128, false>);
-  kern<<<grid, 128, 0, st>>>(A);
-  return last_cuda();
+  if (A.C.d == 64) return i8 ? launch_attend<64, true>(A, st) : launch_attend<64, false>(A, st);
+  return i8 ? launch_attend<128, true>(A, st) : launch_attend<128, false>(A, st);
 }
 
 }  // extern "C"
