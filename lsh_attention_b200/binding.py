@@ -490,6 +490,12 @@ def _cache_rows(B, n, max_pages, batched, xs, vs=(0, 0, 0), os_=(0, 0, 0)) -> Ls
     return LshCacheRows(B, n, max_pages, batched, three(*xs), three(*vs), three(*os_))
 
 
+def _raw_stream(device) -> int:
+    """Handle of the device's current stream: what _stream(None) gives, without making a Stream
+    object (which takes longer than a small kernel)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _on_stream(stream, call, *tensors):
     """Run call() with `stream` current, its results made in that stream's memory; the tensors
     are not handed out again before the stream has passed."""
@@ -524,7 +530,7 @@ def lsh_rope(x, positions, freqs, *, axis_dims, adjacent: bool = False, inverse:
     desc = _rope_desc(B, H, n, d, _DTYPES[x.dtype], int(inverse), batched, axis_dims, adjacent,
                       xs, _rows_strides(out, "out", x.dtype, (B, H, n, d)))
     _check(load().lsh_rope(ctypes.byref(desc), x.data_ptr(), positions.data_ptr(),
-                           freqs.data_ptr(), out.data_ptr(), _stream(None)))
+                           freqs.data_ptr(), out.data_ptr(), _raw_stream(x.device)))
     return out
 
 
@@ -631,7 +637,7 @@ def lsh_cache_append(cache: LshCache, x, v, page_table, seq_len, *, n_valid=None
         ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows),
         ctypes.byref(_axes(axis_dims, adjacent)), x.data_ptr(), v.data_ptr(), _opt(positions),
         _opt(freqs), page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), _opt(xr),
-        _stream(None)))
+        _raw_stream(x.device)))
     return x if xr is None else xr
 
 
@@ -656,7 +662,7 @@ def lsh_cache_gather(cache: LshCache, page_table, start, n: int, *, n_valid=None
     _check(load().lsh_cache_gather(
         ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows),
         page_table.data_ptr(), start.data_ptr(), _opt(n_valid), x.data_ptr(), v.data_ptr(),
-        _stream(None)))
+        _raw_stream(x.device)))
     return x, v
 
 
@@ -687,14 +693,18 @@ def lsh_cache_attend(cache: LshCache, x, page_table, seq_len, *, n_valid=None, o
     rows = _cache_rows(B, n, page_table.shape[1], False, xs, (0, 0, 0),
                        _rows_strides(out, "out", torch.bfloat16, shape))
     need = _attend_workspace(B, n, H, d, cache.page_size, cache.int8)
-    if ws is None:
-        # a graph under capture keeps its own: the cached one may grow and go away
-        ws = (torch.empty(need, dtype=torch.uint8, device=x.device)
-              if torch.cuda.is_current_stream_capturing() else _scratch(x.device, None, need))
+    stream = _raw_stream(x.device)
+    if ws is None and torch.cuda.is_current_stream_capturing():
+        # a graph keeps its own workspace: the cached one may grow and go away
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif ws is None:
+        ws = _ws_cache.get((x.device.index, stream))
+        if ws is None or ws.numel() < need:
+            ws = _scratch(x.device, None, need)
     _check(load().lsh_cache_attend(
         ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows), x.data_ptr(),
         page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), out.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel() * ws.element_size(), _stream(None)))
+        ws.data_ptr(), ws.numel() * ws.element_size(), stream))
     return out, lse
 
 

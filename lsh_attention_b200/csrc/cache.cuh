@@ -93,57 +93,71 @@ struct AppendArgs {
   bf16* xr;  // may be NULL
   int64_t pos_axis, pos_batch;
   int64_t xs[3], vs[3], os[3];
-  int rows;       // tokens a block covers (aligned in the sequence): a multiple
-                  // of 16; int8: the page
   int heads_per;  // heads a block takes one after the other
 };
 
-inline size_t append_smem(int rows, int d, int pairs) {
-  return (size_t)rows * (2 * (d * 2 + 16) + pairs * 8) + 64 * sizeof(float);
+// How the rows are turned.
+enum { kTurnNone = 0, kTurnAdjacent = 1, kTurnRuns = 2, kTurnSingles = 3 };
+
+// Tokens a block covers (aligned in the sequence). bf16 tokens do not depend on
+// one another; int8 ones share their page's scale, so a block has whole pages.
+__host__ __device__ constexpr int append_rows(bool i8, int page) {
+  return !i8 || page < 32 ? 32 : page;
+}
+// Angles of a row in shared memory, rounded up to whole float4.
+__host__ __device__ constexpr int append_pairs(int pairs) { return (pairs + 3) / 4 * 4; }
+constexpr size_t append_smem(int rows, int d, int pairs, int buffers) {
+  return (size_t)rows * (buffers * 2 * (d * 2 + 16) + append_pairs(pairs) * 8) + 128;
 }
 
-// Turn the rows [r0, r1) of `xt` in place, W pairs at a time.
-template <int D, int W, bool ADJ>
-__device__ __forceinline__ void append_rotate(const RotPlan& R, bf16* xt, const float* ct,
-                                              const float* st, int r0, int r1) {
-  constexpr int kSlots = D / (2 * W);
-  for (int i = threadIdx.x; i < (r1 - r0) * kSlots; i += blockDim.x) {
-    const int r = r0 + i / kSlots;
-    int ra, rb, p;
-    rot_slot<W, ADJ>(R, i % kSlots, &ra, &rb, &p);
-    if (p >= R.pairs) continue;
-    bf16* row = xt + r * (D + 8);
-    float u[W], w[W], c[W], s[W];
-    Pack<bf16, W>::load(row + ra, u);
-    Pack<bf16, W>::load(row + rb, w);
+// Tiles of two heads, unless 128 rows of 128 leave room for one.
+constexpr int append_buffers(int d, int rows) { return d * rows > 128 * 64 ? 1 : 2; }
+
+// 1/||x|| of a row whose kLanes lanes hold its values by eight. The row is scaled
+// by a power of two near its largest value, so that no square is lost.
+template <int kLanes>
+__device__ __forceinline__ float inv_norm(const float (&f)[8]) {
+  float m = 0.f, ss = 0.f;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const bool in = p + k < R.pairs;
-      c[k] = in ? ct[r * R.pairs + p + k] : 1.f;
-      s[k] = in ? st[r * R.pairs + p + k] : 0.f;
-    }
-    rot_apply<W, ADJ>(u, w, c, s, R.pairs - p);
-    Pack<bf16, W>::store(row + ra, u);
-    Pack<bf16, W>::store(row + rb, w);
-  }
+  for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  // the exponent of m; 0 for a zero row's and an infinity's
+  const int e = (int)(__float_as_uint(m) >> 23) - 127;
+  const bool plain = e > -127 && e < 127;
+  const float up = plain ? __uint_as_float((uint32_t)(127 - e) << 23) : e > 0 ? 0x1p-126f : 0x1p126f;
+  const float down = plain ? __uint_as_float((uint32_t)(127 + e) << 23) : e > 0 ? 0x1p126f : 0x1p-126f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) ss = fmaf(f[k] * up, f[k] * up, ss);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+  const float norm = sqrtf(ss) * down;
+  return norm < 0x1p-126f ? 0.f : 1.f / norm;
 }
 
-// One block: `rows` consecutive token slots of one sequence (int8: one page) for
-// a few heads. The sines of its tokens are formed once and serve its heads. Per
-// head: rows of x and v into shared memory (cp.async), 1/||x||, rotation in
-// place, the rotated rows out by 16-byte pieces; v leaves through transposed
-// 8x8 tiles (ldmatrix) so that each thread stores four tokens of a dimension
-// together. int8 adds the largest magnitudes over the page in between; this
-// block alone owns the page's head, so an earlier row is re-rounded in place.
-// W: pairs a thread turns together, 0 = none.
+// One block: R consecutive token slots of one sequence for a few heads. The sines
+// of its tokens are formed once and serve its heads; the next head's rows travel
+// (cp.async) while this one's are worked on. A thread takes 16-byte pieces of
+// rows of x: 1/||x||, the rotation with the partners from shared memory, the
+// rotated piece out. v leaves through transposed 8x8 tiles (ldmatrix), so that a
+// thread stores four tokens of a dimension together and a warp whole sectors of
+// the groups. int8: pieces wait in registers for the page's largest magnitude
+// (maxima of non-negative floats by integer atomicMax in shared memory: the same
+// whatever the order); this block alone owns the page's head, so earlier rows
+// are rounded again in place.
 // grid (blocks of rows, head groups, batch), block 256.
-template <int D, bool I8, int W, bool ADJ>
+template <int D, bool I8, int R, int TURN>
 __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   constexpr int kStride = D + 8;  // elements of a shared row: 16 bytes of padding
   constexpr int kPieces = D / 8;  // 16-byte pieces of a row
+  constexpr int kPass = R * kPieces / 256;
+  constexpr int kBuf = append_buffers(D, R);
+  constexpr int W = TURN == kTurnSingles ? 1 : 4;
+  constexpr bool ADJ = TURN == kTurnAdjacent;
+  using P8 = Piece<8, W, ADJ>;
   const CacheView& C = A.C;
   const int b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int T = A.S.n, R = A.rows;
+  const int T = A.S.n;
   const int h0 = blockIdx.y * A.heads_per, h1 = min(h0 + A.heads_per, C.H);
   int len, nv;
   if (!seq_rows(A.S, C.P, b, &len, &nv) && blockIdx.x == 0 && tid == 0) cache_error(C);
@@ -169,126 +183,199 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   const int tok0 = (int)(base - len);  // row r is the call's row tok0 + r
 
   extern __shared__ __align__(16) unsigned char smem[];
-  bf16* xt = reinterpret_cast<bf16*>(smem);
-  bf16* vt = xt + R * kStride;
-  float* ct = reinterpret_cast<float*>(vt + R * kStride);
-  float* st = ct + R * A.rot.pairs;
-  float* red = st + R * A.rot.pairs;  // 2 x 8 maxima, then 2 scales old and new
+  bf16* tiles = reinterpret_cast<bf16*>(smem);  // [buffers][x, v][R][kStride]
+  float* ct = reinterpret_cast<float*>(tiles + kBuf * 2 * R * kStride);
+  const int pstride = append_pairs(A.rot.pairs);
+  float* st = ct + R * pstride;
+  // int8: of at most two pages, largest magnitudes of x and v
+  int* amax = reinterpret_cast<int*>(st + R * pstride);
+  __shared__ int ids[8];  // pages of the block's tokens
+  __shared__ float scales[2][4];  // of a page: x old, new, v old, new
 
-  if constexpr (W > 0) {
+  auto fetch = [&](int h) {
+    bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride;
+    bf16* vt = xt + R * kStride;
+    const int own = (r1 - r0) * kPieces;
+    const bf16* xg = A.x + b * A.xs[0] + h * A.xs[1];
+    const bf16* vg = A.v + b * A.vs[0] + h * A.vs[1];
+    for (int i = tid; i < own; i += 256) {
+      const int r = r0 + i / kPieces, piece = i % kPieces;
+      const int64_t t = tok0 + r;
+      sm100::cp_async16_zfill(xt + r * kStride + piece * 8, xg + t * A.xs[2] + piece * 8, true);
+      sm100::cp_async16_zfill(vt + r * kStride + piece * 8, vg + t * A.vs[2] + piece * 8, true);
+    }
+    sm100::cp_async_commit();
+  };
+  fetch(h0);
+  const int pages = (R + C.P - 1) / C.P;  // a block's tokens lie in this many
+  if (tid < pages) {
+    // the page of the block's tokens from row tid * P on, if it has new ones
+    int id = -1;
+    if (tid * C.P < r1 && (tid + 1) * C.P > r0) {
+      id = page_of(C, A.S, b, (int)((base + tid * C.P) / C.P));
+      if (id < 0 && blockIdx.y == 0) cache_error(C);
+    }
+    ids[tid] = id;
+  }
+  if constexpr (TURN != kTurnNone) {
     const int pairs = A.rot.pairs;
     for (int i = tid; i < (r1 - r0) * pairs; i += 256) {
       const int r = r0 + i / pairs, p = i % pairs;
       const int ax = rot_axis(A.rot, p);
       rot_angle(A.pos[ax * A.pos_axis + b * A.pos_batch + tok0 + r], A.freqs[p],
-                &ct[r * pairs + p], &st[r * pairs + p]);
+                &ct[r * pstride + p], &st[r * pstride + p]);
     }
   }
-  // bad pages: rows of xr are still written, the cache is not
-  for (int r = r0 + tid; r < r1; r += 256)
-    if ((r == r0 || (base + r) % C.P == 0) && page_of(C, A.S, b, (int)((base + r) / C.P)) < 0)
-      cache_error(C);
+  // a thread's pieces are the same dimensions of rows 256 / kPieces apart
+  const int dim0 = tid % kPieces * 8, row0 = tid / kPieces;
+  P8 piece;
+  if constexpr (TURN != kTurnNone) piece.place(A.rot, dim0);
 
   for (int h = h0; h < h1; ++h) {
-    const int own = (r1 - r0) * kPieces;  // pieces of the new rows
-    for (int i = tid; i < own; i += 256) {
-      const int r = r0 + i / kPieces, piece = i % kPieces;
-      const int64_t t = tok0 + r;
-      sm100::cp_async16_zfill(xt + r * kStride + piece * 8,
-                              A.x + b * A.xs[0] + h * A.xs[1] + t * A.xs[2] + piece * 8, true);
-      sm100::cp_async16_zfill(vt + r * kStride + piece * 8,
-                              A.v + b * A.vs[0] + h * A.vs[1] + t * A.vs[2] + piece * 8, true);
+    if (kBuf == 2 && h + 1 < h1) {
+      fetch(h + 1);
+      sm100::cp_async_wait_prev();
+    } else {
+      sm100::cp_async_wait_all();
     }
-    sm100::cp_async_commit();
-    sm100::cp_async_wait_all();
-
-    // 1/||x|| from the pieces this thread has copied: the row scaled by a power
-    // of two near its largest value, so that no square is lost
-    for (int i0 = 0; i0 < own; i0 += 256) {
-      const int i = i0 + tid;
-      const bool in = i < own;
-      const int r = r0 + i / kPieces, piece = i % kPieces;
-      float f[8];
-      if (in) Pack<bf16, 8>::load(xt + r * kStride + piece * 8, f);
-      float m = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = in ? fmaxf(m, fabsf(f[k])) : 0.f;
-#pragma unroll
-      for (int o = kPieces / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-      int e;
-      frexpf(m, &e);
-      e = m > 0.f && m <= 3.4e38f ? max(min(e, 126), -126) : 0;
-      const float up = ldexpf(1.f, -e);
-      float ss = 0.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) ss = in ? fmaf(f[k] * up, f[k] * up, ss) : 0.f;
-#pragma unroll
-      for (int o = kPieces / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-      if (in && piece == 0) {
-        const int id = page_of(C, A.S, b, (int)((base + r) / C.P));
-        const float norm = sqrtf(ss) * ldexpf(1.f, e);
-        if (id >= 0)
-          C.kinv[((int64_t)id * C.H + h) * C.P + (base + r) % C.P] =
-              norm < 1.17549435e-38f ? 0.f : 1.f / norm;
-      }
-    }
+    if (I8 && tid < 4) amax[tid] = 0;
     __syncthreads();
-    if constexpr (W > 0) {
-      append_rotate<D, W, ADJ>(A.rot, xt, ct, st, r0, r1);
-      __syncthreads();
-    }
+    const bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride;
+    const bf16* vt = xt + R * kStride;
+    bf16* xo = A.xr ? A.xr + b * A.os[0] + h * A.os[1] + dim0 : nullptr;
 
-    // the rotated rows: out, and into the cache (bf16)
-    float kmax = 0.f, vmax = 0.f;
-    bool odd = false;
-    for (int i = tid; i < own; i += 256) {
-      const int r = r0 + i / kPieces, piece = i % kPieces;
-      const uint4 u = *reinterpret_cast<const uint4*>(xt + r * kStride + piece * 8);
-      if (A.xr)
-        *reinterpret_cast<uint4*>(A.xr + b * A.os[0] + h * A.os[1] +
-                                  (int64_t)(tok0 + r) * A.os[2] + piece * 8) = u;
-      if constexpr (I8) {
-        float f[8], g[8];
-        Vec16<bf16>::unpack(u, f);
-        Pack<bf16, 8>::load(vt + r * kStride + piece * 8, g);
+    uint4 kept[I8 ? kPass : 1];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const bool fk = fabsf(f[k]) <= 3.4e38f, gk = fabsf(g[k]) <= 3.4e38f;
-          if (fk) kmax = fmaxf(kmax, fabsf(f[k]));
-          if (gk) vmax = fmaxf(vmax, fabsf(g[k]));
+    for (int k = 0; k < kPass; ++k) {
+      const int r = row0 + k * (256 / kPieces);
+      const bool in = r >= r0 && r < r1;
+      const bf16* row = xt + r * kStride;
+      float f[8];
+      uint4 u = *reinterpret_cast<const uint4*>(row + dim0);
+      Vec16<bf16>::unpack(u, f);
+      const float inv = inv_norm<kPieces>(f);
+      const int id = ids[r / C.P];
+      const int slot = (int)(base + r) & (C.P - 1);
+      if (in && id >= 0 && dim0 == 0) C.kinv[((int64_t)id * C.H + h) * C.P + slot] = inv;
+      if constexpr (TURN != kTurnNone) {
+        float y[8], c[P8::kPairs], s[P8::kPairs];
+        if constexpr (ADJ) {
+          load_w<float, 4>(ct + r * pstride + piece.pair[0], c);
+          load_w<float, 4>(st + r * pstride + piece.pair[0], s);
+        } else {
+#pragma unroll
+          for (int q = 0; q < P8::kRuns; ++q) {
+            load_w<bf16, W>(row + piece.other[q], &y[q * W]);
+            load_w<float, W>(ct + r * pstride + piece.pair[q], &c[q * W]);
+            load_w<float, W>(st + r * pstride + piece.pair[q], &s[q * W]);
+#pragma unroll
+            for (int e = 0; e < W; ++e) s[q * W + e] *= piece.sign_of(q * W + e);
+          }
+        }
+        piece.turn(f, y, c, s);
+        u = pack16<bf16>(f);
+      }
+      if (in && xo) *reinterpret_cast<uint4*>(xo + (int64_t)(tok0 + r) * A.os[2]) = u;
+      if constexpr (I8) {
+        kept[k] = u;
+        float g[8];
+        Vec16<bf16>::unpack(u, f);
+        load_w<bf16, 8>(vt + r * kStride + dim0, g);
+        float km = 0.f, vm = 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool fk = fabsf(f[e]) <= 3.4e38f, gk = fabsf(g[e]) <= 3.4e38f;
+          km = fk ? fmaxf(km, fabsf(f[e])) : km;
+          vm = gk ? fmaxf(vm, fabsf(g[e])) : vm;
           odd |= !fk || !gk;
         }
-      } else {
-        const int id = page_of(C, A.S, b, (int)((base + r) / C.P));
-        if (id >= 0)
-          *reinterpret_cast<uint4*>(static_cast<bf16*>(C.k) + page_base(C, id, h) +
-                                    (base + r) % C.P * D + piece * 8) = u;
+        if (!in) km = vm = 0.f;
+        if (in && odd) cache_error(C);
+        // a warp's rows of a pass lie in one page of 16 at least
+        km = warp_max(km);
+        vm = warp_max(vm);
+        if (lane == 0) {
+          atomicMax(&amax[2 * (r / C.P)], __float_as_int(km));
+          atomicMax(&amax[2 * (r / C.P) + 1], __float_as_int(vm));
+        }
+      } else if (in && id >= 0) {
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(C.k) + page_base(C, id, h) + slot * D + dim0) = u;
       }
     }
 
-    if constexpr (!I8) {
-      // v: warps take the block's groups of 16 tokens, 32 dimensions a step
-      const int g0 = r0 / kGroup, g1 = (r1 - 1) / kGroup;
-      constexpr int kSteps = D / 16;
-      for (int w = warp; w < (g1 - g0 + 1) * kSteps; w += 8) {
-        const int grp = g0 + w / kSteps, dim0 = (w % kSteps) * 16;
-        const int rb = grp * kGroup;
-        // tiles 0, 1: tokens {0,1,4,5,8,9,12,13} and {2,3,6,7,10,11,14,15} of
-        // dimensions dim0..; tiles 2, 3 the same of the next eight: lane (g, t)
-        // then holds tokens 4t .. 4t + 3 of dimensions dim0 + g and dim0 + 8 + g
-        const int i = lane & 7, tile = lane >> 3;
-        const int trow = rb + (i >> 1) * 4 + (i & 1) + 2 * (tile & 1);
-        uint32_t m[4];
-        ldsm_x4_trans(m, vt + trow * kStride + dim0 + 8 * (tile >> 1));
-        const int64_t at = base + rb;
-        const int id = page_of(C, A.S, b, (int)(at / C.P));
-        if (id < 0) continue;
-        bf16* dst = static_cast<bf16*>(C.v) + page_base(C, id, h) +
-                    at % C.P * D + (dim0 + (lane >> 2)) * kGroup + (lane & 3) * 4;
-        const int tk = rb + (lane & 3) * 4;
+    bool again = false;  // int8: some page's earlier rows are rounded again
+    if constexpr (I8) {
+      __syncthreads();
+      if (tid < 2 * pages) {
+        // rows before r0 belong to the block's first new page at most, and are
+        // old ones of the page if it starts before them
+        const int pg = tid >> 1, id = ids[pg];
+        float was = 0.f, now = 0x1p-126f;
+        if (id >= 0) {
+          float* sc = (tid & 1 ? C.vscale : C.kscale) + (int64_t)id * C.H + h;
+          if (r0 > pg * C.P) was = *sc;
+          now = fmaxf(was, scale_for(__int_as_float(amax[tid])));
+          if (now != was) *sc = now;
+        }
+        scales[pg][2 * (tid & 1)] = was;
+        scales[pg][2 * (tid & 1) + 1] = now;
+      }
+      __syncthreads();
+      const int pf = r0 / C.P;  // the page that may have earlier rows
+      const int old = r0 - pf * C.P, id = ids[pf];
+      again = old > 0 && id >= 0 && scales[pf][3] != scales[pf][2];
+      if (old > 0 && id >= 0 && scales[pf][1] != scales[pf][0]) {
+        int8_t* kp = static_cast<int8_t*>(C.k) + page_base(C, id, h);
+        const float f = scales[pf][0] / scales[pf][1];  // a power of two
+        for (int i = tid; i < old * D / 4; i += 256) {
+          char4 q = *reinterpret_cast<char4*>(kp + 4 * i);
+          q.x = (signed char)rintf(q.x * f);
+          q.y = (signed char)rintf(q.y * f);
+          q.z = (signed char)rintf(q.z * f);
+          q.w = (signed char)rintf(q.w * f);
+          *reinterpret_cast<char4*>(kp + 4 * i) = q;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kPass; ++k) {
+        const int r = row0 + k * (256 / kPieces), id = ids[r / C.P];
+        if (r < r0 || r >= r1 || id < 0) continue;
+        const float rs = 1.f / scales[r / C.P][1];
+        float f[8];
+        Vec16<bf16>::unpack(kept[k], f);
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)(quant(f[e], rs) & 255) << (8 * (e & 3));
+        const int slot = (int)(base + r) & (C.P - 1);
+        *reinterpret_cast<uint2*>(static_cast<int8_t*>(C.k) + page_base(C, id, h) + slot * D + dim0) =
+            make_uint2(w[0], w[1]);
+      }
+    }
+
+    // v: warps take (group of 16 tokens, 16 dimensions) in turn
+    constexpr int kSteps = D / 16;
+    const int g0 = again ? r0 / C.P * C.P / kGroup : r0 / kGroup, g1 = (r1 - 1) / kGroup;
+    for (int w = warp; w < (g1 - g0 + 1) * kSteps; w += 8) {
+      const int rb = (g0 + w / kSteps) * kGroup, d0 = (w % kSteps) * 16;
+      // tiles 0, 1: tokens {0,1,4,5,8,9,12,13} and {2,3,6,7,10,11,14,15} of
+      // dimensions d0 ..; tiles 2, 3 the same of the next eight: lane (g, t) then
+      // holds tokens 4t .. 4t + 3 of dimensions d0 + g and d0 + 8 + g
+      const int i = lane & 7, tile = lane >> 3;
+      const int trow = rb + (i >> 1) * 4 + (i & 1) + 2 * (tile & 1);
+      uint32_t m[4];
+      ldsm_x4_trans(m, vt + trow * kStride + d0 + 8 * (tile >> 1));
+      const int id = ids[rb / C.P];
+      if (id < 0) continue;
+      const int64_t at = page_base(C, id, h) + ((base + rb) & (C.P - 1)) * D +
+                         (d0 + (lane >> 2)) * kGroup + (lane & 3) * 4;
+      const int tk = rb + (lane & 3) * 4;
+      const bool all = tk >= r0 && tk + 4 <= r1;
+      if constexpr (!I8) {
+        bf16* dst = static_cast<bf16*>(C.v) + at;
 #pragma unroll
         for (int k = 0; k < 2; ++k, dst += 8 * kGroup) {
-          if (tk >= r0 && tk + 4 <= r1) {
+          if (all) {
             *reinterpret_cast<uint2*>(dst) = make_uint2(m[2 * k], m[2 * k + 1]);
           } else {
             uint16_t* e = reinterpret_cast<uint16_t*>(dst);
@@ -298,91 +385,31 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
                 e[q] = (uint16_t)(m[2 * k + (q >> 1)] >> (16 * (q & 1)));
           }
         }
-      }
-    } else {
-      if (__syncthreads_or(odd) && tid == 0) cache_error(C);
-      kmax = warp_max(kmax);
-      vmax = warp_max(vmax);
-      if (lane == 0) {
-        red[warp] = kmax;
-        red[8 + warp] = vmax;
-      }
-      __syncthreads();
-      const int id = page_of(C, A.S, b, (int)(base / C.P));
-      if (id >= 0) {
-        const int64_t hs = (int64_t)id * C.H + h;
-        if (tid < 2) {
-          float m = 0.f;
-          for (int k = 0; k < 8; ++k) m = fmaxf(m, red[8 * tid + k]);
-          float* sc = tid ? C.vscale : C.kscale;
-          const float was = r0 > 0 ? sc[hs] : 0.f;
-          const float now = fmaxf(was, scale_for(m));
-          if (now != was) sc[hs] = now;
-          red[16 + 2 * tid] = was;
-          red[17 + 2 * tid] = now;
-        }
-      }
-      __syncthreads();
-      if (id >= 0) {
-        const float kwas = red[16], know = red[17], vwas = red[18], vnow = red[19];
-        int8_t* kp = static_cast<int8_t*>(C.k) + page_base(C, id, h);
-        int8_t* vp = static_cast<int8_t*>(C.v) + page_base(C, id, h);
-        const float krs = 1.f / know, vrs = 1.f / vnow;
-        // earlier rows of the page at the raised scale (the ratio is a power of two)
-        if (r0 > 0 && know != kwas) {
-          const float f = kwas * krs;
-          for (int i = tid; i < r0 * D / 4; i += 256) {
-            char4 q = *reinterpret_cast<char4*>(kp + 4 * i);
-            q.x = (signed char)rintf(q.x * f);
-            q.y = (signed char)rintf(q.y * f);
-            q.z = (signed char)rintf(q.z * f);
-            q.w = (signed char)rintf(q.w * f);
-            *reinterpret_cast<char4*>(kp + 4 * i) = q;
+      } else {
+        int8_t* dst = static_cast<int8_t*>(C.v) + at;
+        const float rs = 1.f / scales[rb / C.P][3];
+        const bool redo = again && tk < r0;
+        const float vf = redo ? scales[rb / C.P][2] * rs : 1.f;
+        if (tk >= r1 || (tk + 4 <= r0 && !redo)) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k, dst += 8 * kGroup) {
+          char4 q = make_char4(0, 0, 0, 0);
+          if (!all) q = *reinterpret_cast<char4*>(dst);
+          signed char* e = reinterpret_cast<signed char*>(&q);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t mw = m[2 * k + (j >> 1)];
+            if (tk + j >= r0 && tk + j < r1)
+              e[j] = (signed char)quant(j & 1 ? bf_hi(mw) : bf_lo(mw), rs);
+            else if (tk + j < r0 && redo)
+              e[j] = (signed char)rintf(e[j] * vf);
           }
-        }
-        for (int i = tid; i < own; i += 256) {
-          const int r = r0 + i / kPieces, piece = i % kPieces;
-          float f[8];
-          Pack<bf16, 8>::load(xt + r * kStride + piece * 8, f);
-          uint32_t w[2] = {0, 0};
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            w[k >> 2] |= (uint32_t)(quant(f[k], krs) & 255) << (8 * (k & 3));
-          *reinterpret_cast<uint2*>(kp + r * D + piece * 8) = make_uint2(w[0], w[1]);
-        }
-        const bool again = r0 > 0 && vnow != vwas;
-        const float vf = vwas * vrs;
-        const int g0 = again ? 0 : r0 / kGroup, g1 = (r1 - 1) / kGroup;
-        constexpr int kSteps = D / 16;
-        for (int w = warp; w < (g1 - g0 + 1) * kSteps; w += 8) {
-          const int grp = g0 + w / kSteps, dim0 = (w % kSteps) * 16;
-          const int rb = grp * kGroup;
-          const int i = lane & 7, tile = lane >> 3;
-          const int trow = rb + (i >> 1) * 4 + (i & 1) + 2 * (tile & 1);
-          uint32_t m[4];
-          ldsm_x4_trans(m, vt + trow * kStride + dim0 + 8 * (tile >> 1));
-          int8_t* dst = vp + rb * D + (dim0 + (lane >> 2)) * kGroup + (lane & 3) * 4;
-          const int tk = rb + (lane & 3) * 4;
-#pragma unroll
-          for (int k = 0; k < 2; ++k, dst += 8 * kGroup) {
-            if (tk >= r1 || (tk + 4 <= r0 && !again)) continue;
-            char4 q = make_char4(0, 0, 0, 0);
-            if (tk < r0 || tk + 4 > r1) q = *reinterpret_cast<char4*>(dst);
-            signed char* e = reinterpret_cast<signed char*>(&q);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t mw = m[2 * k + (j >> 1)];
-              if (tk + j >= r0 && tk + j < r1)
-                e[j] = (signed char)quant(j & 1 ? bf_hi(mw) : bf_lo(mw), vrs);
-              else if (tk + j < r0 && again)
-                e[j] = (signed char)rintf(e[j] * vf);
-            }
-            *reinterpret_cast<char4*>(dst) = q;
-          }
+          *reinterpret_cast<char4*>(dst) = q;
         }
       }
     }
-    __syncthreads();  // the tiles are free for the next head
+    __syncthreads();  // the tile is free
+    if (kBuf == 1 && h + 1 < h1) fetch(h + 1);
   }
 }
 

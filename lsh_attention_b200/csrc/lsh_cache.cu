@@ -4,6 +4,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
+#include <utility>
 
 #include "cache.cuh"
 #include "cache_attend.cuh"
@@ -65,28 +67,47 @@ lsh_status check_rot(const lsh_rope_axes* rot, int d, RotPlan* R) {
   return LSH_OK;
 }
 
-// Pairs a thread turns together: a run of them fills at most 16 bytes. Adjacent
-// pairs always do. Pairs of halves lie in two runs that have to stay inside
-// their axis, so the width divides every axis's pairs (24 dimensions: 12 pairs,
-// runs of 4, 8 bytes).
-int rot_width(const RotPlan& R, int esize) {
-  int w = 16 / esize;
-  if (!R.adjacent)
-    for (int a = 0; a < R.axes; ++a)
-      while (R.half[a] % w != 0) w /= 2;
+// Partners of halves lie in runs that have to stay inside their axis: the widest
+// run, up to 16 bytes, that divides every axis's pairs (24 dimensions: 12 pairs,
+// runs of 4).
+int run_width(const RotPlan& R, int most) {
+  int w = most;
+  for (int a = 0; a < R.axes; ++a)
+    while (R.half[a] % w != 0) w /= 2;
   return w;
 }
 
-template <typename T, int W>
-lsh_status launch_rope_w(const RopeArgs& A, const void* x, void* out, cudaStream_t st) {
-  const int64_t threads = (int64_t)A.n * (A.d / (2 * W));
-  const int64_t blocks = (threads + 255) / 256;
+template <typename T, int D>
+lsh_status launch_rope(const RopeArgs& A, const void* x, void* out, cudaStream_t st) {
+  constexpr int N = 16 / sizeof(T);
+  const int64_t blocks = ((int64_t)A.n * (D / N) + 255) / 256;
   const dim3 grid((unsigned)blocks, (unsigned)std::min<int64_t>((int64_t)A.B * A.head_groups, 65535));
-  auto kern = k_rope<T, W, false>;
-  if constexpr (W * sizeof(T) == 16)  // adjacent pairs always come by 16 bytes
-    if (A.rot.adjacent) kern = k_rope<T, W, true>;
+  auto kern = k_rope<T, D, 1, false>;
+  if (A.rot.adjacent) {
+    kern = k_rope<T, D, 1, true>;
+  } else {
+    const int w = run_width(A.rot, N);
+    if (w == N) kern = k_rope<T, D, N, false>;
+    else if (w == 4) kern = k_rope<T, D, 4, false>;
+    else if (w == 2) kern = k_rope<T, D, 2, false>;
+  }
   kern<<<grid, 256, 0, st>>>(static_cast<const T*>(x), static_cast<T*>(out), A);
   return last_cuda();
+}
+
+// Shared memory of a kernel raised to `bytes`, once for each device: `done` is
+// the kernel's own record. (The call costs about as much as a small launch.)
+template <typename K>
+bool allow_smem(K kern, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) !=
+      cudaSuccess)
+    return false;
+  done->fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 // ---------------------------------------------------------------- cache calls
@@ -115,28 +136,33 @@ lsh_status check_cache(const lsh_cache_desc* c, const lsh_cache* m, const lsh_ca
   return LSH_OK;
 }
 
-template <int D, bool I8, int W, bool ADJ>
-lsh_status launch_append_w(const AppendArgs& A, cudaStream_t st) {
-  const size_t smem = append_smem(A.rows, D, A.rot.pairs);
-  auto kern = k_cache_append<D, I8, W, ADJ>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-      cudaSuccess)
-    return LSH_ERR_CUDA;
-  const dim3 grid((unsigned)((A.S.n + A.rows - 2) / A.rows + 1),
+template <int D, bool I8, int R, int TURN>
+lsh_status launch_append_t(const AppendArgs& A, cudaStream_t st) {
+  constexpr int kBuf = append_buffers(D, R);
+  auto kern = k_cache_append<D, I8, R, TURN>;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, (int)append_smem(R, D, D / 2, kBuf), &done)) return LSH_ERR_CUDA;
+  const dim3 grid((unsigned)((A.S.n + R - 2) / R + 1),
                   (unsigned)((A.C.H + A.heads_per - 1) / A.heads_per), (unsigned)A.S.B);
-  kern<<<grid, 256, smem, st>>>(A);
+  kern<<<grid, 256, append_smem(R, D, A.rot.pairs, kBuf), st>>>(A);
   return last_cuda();
 }
 
-template <int D, bool I8>
-lsh_status launch_append(const AppendArgs& A, cudaStream_t st) {
-  if (A.rot.axes == 0) return launch_append_w<D, I8, 0, false>(A, st);
-  if (A.rot.adjacent) return launch_append_w<D, I8, 8, true>(A, st);
-  switch (rot_width(A.rot, 2)) {
-    case 8: return launch_append_w<D, I8, 8, false>(A, st);
-    case 4: return launch_append_w<D, I8, 4, false>(A, st);
-    case 2: return launch_append_w<D, I8, 2, false>(A, st);
-    default: return launch_append_w<D, I8, 1, false>(A, st);
+template <int D, bool I8, int R>
+lsh_status launch_append_r(const AppendArgs& A, cudaStream_t st) {
+  if (A.rot.axes == 0) return launch_append_t<D, I8, R, kTurnNone>(A, st);
+  if (A.rot.adjacent) return launch_append_t<D, I8, R, kTurnAdjacent>(A, st);
+  if (run_width(A.rot, 4) == 4) return launch_append_t<D, I8, R, kTurnRuns>(A, st);
+  return launch_append_t<D, I8, R, kTurnSingles>(A, st);
+}
+
+template <int D>
+lsh_status launch_append(const AppendArgs& A, bool i8, cudaStream_t st) {
+  if (!i8) return launch_append_r<D, false, append_rows(false, 0)>(A, st);
+  switch (append_rows(true, A.C.P)) {
+    case 32: return launch_append_r<D, true, 32>(A, st);
+    case 64: return launch_append_r<D, true, 64>(A, st);
+    default: return launch_append_r<D, true, 128>(A, st);
   }
 }
 
@@ -164,9 +190,8 @@ lsh_status launch_attend(const AttendArgs& A, cudaStream_t st) {
   static_assert(Cfg::kStages >= 3 && Cfg::kStages <= 8, "ring");
   static_assert(sizeof(TileMeta) <= Cfg::kMeta, "stage header");
   auto kern = k_cache_attend<D, I8>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem) !=
-      cudaSuccess)
-    return LSH_ERR_CUDA;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, Cfg::kSmem, &done)) return LSH_ERR_CUDA;
   const unsigned blocks = (unsigned)attend_layout(D).blocks;
   kern<<<blocks, kAttThreads, Cfg::kSmem, st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
@@ -211,7 +236,6 @@ lsh_status lsh_rope(const lsh_rope_desc* desc, const void* x, const int32_t* pos
   A.B = q.batch;
   A.H = q.heads;
   A.n = q.n;
-  A.d = q.d;
   A.pos_axis = q.pos_batched ? (int64_t)q.batch * q.n : q.n;
   A.pos_batch = q.pos_batched ? q.n : 0;
   for (int i = 0; i < 3; ++i) {
@@ -219,27 +243,17 @@ lsh_status lsh_rope(const lsh_rope_desc* desc, const void* x, const int32_t* pos
     A.os[i] = q.out_stride[i];
   }
   A.sign = q.inverse ? -1.f : 1.f;
-  const int w = rot_width(A.rot, esize);
   // heads are split over blocks until the card is filled
-  const int64_t blocks = ((int64_t)q.n * (q.d / (2 * w)) + 255) / 256 * q.batch;
+  const int64_t blocks = ((int64_t)q.n * (q.d * esize / 16) + 255) / 256 * q.batch;
   const int64_t want = 8 * sm_count();
-  int groups = (int)std::min<int64_t>(q.heads, std::max<int64_t>(1, want / std::max<int64_t>(blocks, 1)));
+  const int groups = (int)std::min<int64_t>(q.heads, std::max<int64_t>(1, want / blocks));
   A.heads_per = (q.heads + groups - 1) / groups;
   A.head_groups = (q.heads + A.heads_per - 1) / A.heads_per;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (q.dtype == LSH_BF16) {
-    switch (w) {
-      case 8: return launch_rope_w<__nv_bfloat16, 8>(A, x, out, st);
-      case 4: return launch_rope_w<__nv_bfloat16, 4>(A, x, out, st);
-      case 2: return launch_rope_w<__nv_bfloat16, 2>(A, x, out, st);
-      default: return launch_rope_w<__nv_bfloat16, 1>(A, x, out, st);
-    }
-  }
-  switch (w) {
-    case 4: return launch_rope_w<float, 4>(A, x, out, st);
-    case 2: return launch_rope_w<float, 2>(A, x, out, st);
-    default: return launch_rope_w<float, 1>(A, x, out, st);
-  }
+  if (q.dtype == LSH_BF16)
+    return q.d == 64 ? launch_rope<__nv_bfloat16, 64>(A, x, out, st)
+                     : launch_rope<__nv_bfloat16, 128>(A, x, out, st);
+  return q.d == 64 ? launch_rope<float, 64>(A, x, out, st) : launch_rope<float, 128>(A, x, out, st);
 }
 
 lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
@@ -272,14 +286,13 @@ lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
     A.os[i] = rows->out_stride[i];
   }
   const bool i8 = desc->format == LSH_CACHE_I8;
-  A.rows = i8 ? A.C.P : 32;
-  const int64_t blocks = (int64_t)((A.S.n + A.rows - 2) / A.rows + 1) * A.S.B;
-  const int64_t want = 8 * sm_count();
+  const int rows_per = append_rows(i8, A.C.P);
+  const int64_t blocks = (int64_t)((A.S.n + rows_per - 2) / rows_per + 1) * A.S.B;
+  const int64_t want = 16 * sm_count();
   const int groups = (int)std::min<int64_t>(A.C.H, std::max<int64_t>(1, want / blocks));
   A.heads_per = (A.C.H + groups - 1) / groups;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (A.C.d == 64) return i8 ? launch_append<64, true>(A, st) : launch_append<64, false>(A, st);
-  return i8 ? launch_append<128, true>(A, st) : launch_append<128, false>(A, st);
+  return A.C.d == 64 ? launch_append<64>(A, i8, st) : launch_append<128>(A, i8, st);
 }
 
 lsh_status lsh_cache_gather(const lsh_cache_desc* desc, const lsh_cache* cache,

@@ -36,86 +36,100 @@ __device__ __forceinline__ void rot_angle(int32_t pos, float freq, float* c, flo
   sincospif(2.0f * (float)turns, s, c);
 }
 
-// W consecutive elements of T, loaded and stored as one access, as fp32.
+// W consecutive elements of T (W = 1 too), loaded as one access, as fp32.
 template <typename T, int W>
-struct Pack {
-  static constexpr int kBytes = W * (int)sizeof(T);
-  static __device__ __forceinline__ void load(const T* p, float* f) {
-    if constexpr (kBytes == 16) {
-      Vec16<T>::unpack(*reinterpret_cast<const uint4*>(p), f);
-    } else {
-      alignas(16) T e[W];
-      if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
-      else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
-      else e[0] = p[0];
+__device__ __forceinline__ void load_w(const T* p, float* f) {
+  constexpr int kBytes = W * (int)sizeof(T);
+  if constexpr (kBytes == 16) {
+    Vec16<T>::unpack(*reinterpret_cast<const uint4*>(p), f);
+  } else {
+    alignas(8) T e[W];
+    if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
+    else e[0] = p[0];
 #pragma unroll
-      for (int i = 0; i < W; ++i) f[i] = Elem<T>::to_f(e[i]);
+    for (int i = 0; i < W; ++i) f[i] = Elem<T>::to_f(e[i]);
+  }
+}
+// fp32 values rounded to T, 16 bytes.
+template <typename T>
+__device__ __forceinline__ uint4 pack16(const float* f) {
+  alignas(16) T e[16 / sizeof(T)];
+#pragma unroll
+  for (int i = 0; i < 16 / (int)sizeof(T); ++i) e[i] = Elem<T>::from_f(f[i]);
+  return *reinterpret_cast<uint4*>(e);
+}
+
+// A thread turns a piece of N consecutive dimensions (16 bytes), so rows are read
+// and written by whole sectors whatever the axes are. It needs the pairs' other
+// dimensions too: neighbouring pairs lie inside the piece (ADJ); of halves the
+// others lie in runs of W dimensions, which a lane of the same row holds. W
+// divides every axis's pairs, so a run's partners are a run.
+template <int N, int W, bool ADJ>
+struct Piece {
+  static constexpr int kRuns = ADJ ? 1 : N / W;
+  static constexpr int kPairs = ADJ ? N / 2 : N;  // angles
+  int other[kRuns];       // halves: first partner dimension of each run
+  int pair[kRuns];        // first pair of each run
+  uint32_t first, turned;  // bit per run: first half; bit per angle: is rotated
+
+  __device__ __forceinline__ void place(const RotPlan& R, int dim0) {
+    first = turned = 0;
+    if constexpr (ADJ) {
+      pair[0] = dim0 / 2;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) turned |= (uint32_t)(pair[0] + i < R.pairs) << i;
+      if (!turned) pair[0] = 0;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kRuns; ++k) {
+        const int dim = dim0 + k * W;
+        other[k] = dim;
+        pair[k] = 0;
+        if (dim >= 2 * R.pairs) continue;
+        int a = 0;
+#pragma unroll
+        for (int i = 1; i < LSH_ROPE_MAX_AXES; ++i)
+          if (i < R.axes && dim >= R.off[i]) a = i;
+        const int at = dim - R.off[a], h = R.half[a];
+        const bool lo = at < h;
+        other[k] = lo ? dim + h : dim - h;
+        pair[k] = R.off[a] / 2 + (lo ? at : at - h);
+        first |= (uint32_t)lo << k;
+        turned |= ((1u << W) - 1) << (k * W);
+      }
     }
   }
-  static __device__ __forceinline__ void store(T* p, const float* f) {
-    alignas(16) T e[W];
+  // pair of angle i, and the sign its sine takes
+  __device__ __forceinline__ int pair_of(int i) const { return ADJ ? pair[0] + i : pair[i / W] + i % W; }
+  __device__ __forceinline__ float sign_of(int i) const {
+    return !ADJ && (first >> (i / W) & 1) ? -1.f : 1.f;
+  }
+  // x: the piece; y: its partners (halves); c, s: of every angle, s signed.
+  // Spelled out, so that every kernel rounds alike; what is not turned is copied,
+  // not multiplied: it may be infinite.
+  __device__ __forceinline__ void turn(float (&x)[N], const float (&y)[N], const float (&c)[kPairs],
+                                       const float (&s)[kPairs]) const {
 #pragma unroll
-    for (int i = 0; i < W; ++i) e[i] = Elem<T>::from_f(f[i]);
-    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<uint4*>(e);
-    else if constexpr (kBytes == 8) *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(e);
-    else if constexpr (kBytes == 4) *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<uint32_t*>(e);
-    else p[0] = e[0];
+    for (int i = 0; i < kPairs; ++i) {
+      if (!(turned >> i & 1)) continue;
+      if constexpr (ADJ) {
+        const float lo = x[2 * i], hi = x[2 * i + 1];
+        x[2 * i] = __fmaf_rn(lo, c[i], __fmul_rn(hi, -s[i]));
+        x[2 * i + 1] = __fmaf_rn(hi, c[i], __fmul_rn(lo, s[i]));
+      } else {
+        x[i] = __fmaf_rn(x[i], c[i], __fmul_rn(y[i], s[i]));
+      }
+    }
   }
 };
-
-// Slot s of a row, s < d / (2 W): W pairs, held in two runs of W dimensions
-// that start at *a and *b. Pairing by halves: the runs are the pairs' first and
-// second dimensions (W divides every axis's pairs, so a run stays in its axis);
-// adjacent: the runs follow one another and hold both. *first is the number of
-// the first pair; pairs from r.pairs on are not rotated.
-template <int W, bool ADJ>
-__device__ __forceinline__ void rot_slot(const RotPlan& r, int s, int* a, int* b, int* first) {
-  const int p = s * W;
-  *first = p;
-  if (ADJ || p >= r.pairs) {
-    *a = 2 * p;
-    *b = 2 * p + W;
-  } else {
-    const int ax = rot_axis(r, p);
-    *a = r.off[ax] / 2 + p;  // off + (p - off / 2)
-    *b = *a + r.half[ax];
-  }
-}
-
-// The first `turned` of a slot's W pairs turned by (c, s) in place, the others
-// left as they are (not multiplied: they may hold infinities): x of run a, y of
-// run b.
-template <int W, bool ADJ>
-__device__ __forceinline__ void rot_apply(float (&x)[W], float (&y)[W], const float (&c)[W],
-                                          const float (&s)[W], int turned) {
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if (i >= turned) continue;
-    float lo, hi;
-    if (ADJ && W > 1) {
-      lo = 2 * i < W ? x[(2 * i) % W] : y[(2 * i) % W];
-      hi = 2 * i + 1 < W ? x[(2 * i + 1) % W] : y[(2 * i + 1) % W];
-    } else {
-      lo = x[i];
-      hi = y[i];
-    }
-    const float l2 = lo * c[i] - hi * s[i], h2 = lo * s[i] + hi * c[i];
-    if (ADJ && W > 1) {
-      (2 * i < W ? x[(2 * i) % W] : y[(2 * i) % W]) = l2;
-      (2 * i + 1 < W ? x[(2 * i + 1) % W] : y[(2 * i + 1) % W]) = h2;
-    } else {
-      x[i] = l2;
-      y[i] = h2;
-    }
-  }
-}
 
 constexpr int kRopeHeads = 4;  // heads loaded together by a thread
 
 struct RopeArgs {
   const int32_t* pos;
   const float* freqs;
-  int B, H, n, d;
+  int B, H, n;
   int heads_per;       // heads a thread turns with the same sines
   int head_groups;
   int64_t pos_axis, pos_batch;  // strides of positions
@@ -124,51 +138,62 @@ struct RopeArgs {
   RotPlan rot;
 };
 
-// One thread holds a token's slot: its W sines and cosines serve every head of
-// its group, so that the angles cost a fraction 1/heads_per of the rows.
-// grid (blocks over tokens x slots, batch x head groups), block 256.
-template <typename T, int W, bool ADJ>
+// One thread holds a piece of a token: its sines and cosines serve every head of
+// its group, so that the angles cost a fraction 1 / heads_per of the rows. Bound
+// by DRAM: what counts is whole sectors and bytes in flight, four heads' pieces
+// a thread.
+// grid (blocks over tokens x pieces, batch x head groups), block 256.
+template <typename T, int D, int W, bool ADJ>
 __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
-  const int slots = A.d / (2 * W);
-  const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  const int64_t tok = id / slots;
-  const int slot = (int)(id - tok * slots);
-  if (tok >= A.n) return;
+  constexpr int N = 16 / sizeof(T), kPieces = D / N;  // a row's pieces lie in one warp
+  using P = Piece<N, W, ADJ>;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t tok = id / kPieces;
+  const int dim0 = (int)(id % kPieces) * N;
+  const bool in = tok < A.n;
+  P piece;
+  piece.place(A.rot, dim0);
   for (int64_t bg = blockIdx.y; bg < (int64_t)A.B * A.head_groups; bg += gridDim.y) {
     const int b = (int)(bg / A.head_groups), h0 = (int)(bg % A.head_groups) * A.heads_per;
     const int h1 = min(h0 + A.heads_per, A.H);
-    int ra, rb, p;
-    rot_slot<W, ADJ>(A.rot, slot, &ra, &rb, &p);
-    float c[W], s[W];
+    const T* xp = x + b * A.xs[0] + (in ? tok : 0) * A.xs[2];
+    T* op = out + b * A.os[0] + tok * A.os[2] + dim0;
+    float c[P::kPairs], s[P::kPairs];
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+    for (int i = 0; i < P::kPairs; ++i) {
       c[i] = 1.f;
       s[i] = 0.f;
-      if (p + i < A.rot.pairs) {
-        const int ax = rot_axis(A.rot, p + i);
-        rot_angle(A.pos[ax * A.pos_axis + b * A.pos_batch + tok], A.freqs[p + i], &c[i], &s[i]);
-        s[i] *= A.sign;
+      if (in && (piece.turned >> i & 1)) {
+        const int p = piece.pair_of(i);
+        rot_angle(A.pos[rot_axis(A.rot, p) * A.pos_axis + b * A.pos_batch + tok], A.freqs[p], &c[i],
+                  &s[i]);
+        s[i] *= A.sign * piece.sign_of(i);
       }
     }
-    const int turned = A.rot.pairs - p;
-    const T* xp = x + b * A.xs[0] + tok * A.xs[2];
-    T* op = out + b * A.os[0] + tok * A.os[2];
-    // heads in batches, all of a batch loaded before the first is stored: x and
-    // out may be the same rows, so the compiler cannot do this by itself
+    // heads in batches, all of a batch loaded before the first is stored; x and
+    // out may be the same rows, so a warp's partners are read before any lane
+    // writes
     for (int h = h0; h < h1; h += kRopeHeads) {
-      float u[kRopeHeads][W], w[kRopeHeads][W];
+      uint4 u[kRopeHeads];
+      float y[kRopeHeads][N];
 #pragma unroll
       for (int k = 0; k < kRopeHeads; ++k)
         if (h + k < h1) {
-          Pack<T, W>::load(xp + (h + k) * A.xs[1] + ra, u[k]);
-          Pack<T, W>::load(xp + (h + k) * A.xs[1] + rb, w[k]);
+          const T* row = xp + (h + k) * A.xs[1];
+          u[k] = *reinterpret_cast<const uint4*>(row + dim0);
+          if constexpr (!ADJ) {
+#pragma unroll
+            for (int r = 0; r < P::kRuns; ++r) load_w<T, W>(row + piece.other[r], &y[k][r * W]);
+          }
         }
+      __syncwarp();
 #pragma unroll
       for (int k = 0; k < kRopeHeads; ++k)
-        if (h + k < h1) {
-          rot_apply<W, ADJ>(u[k], w[k], c, s, turned);
-          Pack<T, W>::store(op + (h + k) * A.os[1] + ra, u[k]);
-          Pack<T, W>::store(op + (h + k) * A.os[1] + rb, w[k]);
+        if (h + k < h1 && in) {
+          float f[N];
+          Vec16<T>::unpack(u[k], f);
+          piece.turn(f, y[k], c, s);
+          *reinterpret_cast<uint4*>(op + (h + k) * A.os[1]) = pack16<T>(f);
         }
     }
   }
