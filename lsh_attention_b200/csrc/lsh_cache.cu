@@ -187,16 +187,20 @@ AttendLayout attend_layout(int d) {
 template <int D, bool I8>
 lsh_status launch_attend(const AttendArgs& A, cudaStream_t st) {
   using Cfg = AttCfg<D, I8>;
-  static_assert(Cfg::kStages >= 3 && Cfg::kStages <= 8, "ring");
-  static_assert(sizeof(TileMeta) <= Cfg::kMeta, "stage header");
+  static_assert(Cfg::kStages >= kAttWarps && Cfg::kStages <= 16 && Cfg::kStages % 2 == 0, "ring");
+  // those of the two batches looked up and of the ring: a joined segment has two
+  // units at least
+  static_assert(kSegRing > Cfg::kStages / 2 + 3, "segments in flight");
+  static_assert(sizeof(UnitMeta) <= 128 && Cfg::kStage % 16 == 0, "stage header");
+  static_assert(128 * 4 + 2 * 16 * 8 + kSegRing * sizeof(SegInfo) <= 2048, "fixed part");
   auto kern = k_cache_attend<D, I8>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, Cfg::kSmem, &done)) return LSH_ERR_CUDA;
   const unsigned blocks = (unsigned)attend_layout(D).blocks;
   kern<<<blocks, kAttThreads, Cfg::kSmem, st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
-  // a table that holds one tile at most leaves nothing to join
-  if ((int64_t)A.S.max_pages * A.C.P <= kTileTok) return LSH_OK;
+  // a table that holds one unit at most leaves nothing to join
+  if ((int64_t)A.S.max_pages * A.C.P <= Cfg::kTok) return LSH_OK;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;

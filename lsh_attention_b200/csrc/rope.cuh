@@ -141,60 +141,82 @@ struct RopeArgs {
 // One thread holds a piece of a token: its sines and cosines serve every head of
 // its group, so that the angles cost a fraction 1 / heads_per of the rows. Bound
 // by DRAM: what counts is whole sectors and bytes in flight, four heads' pieces
-// a thread.
+// a thread. Halves: the lanes of a row form each angle once and share them, and
+// pass one another their pieces, through shared memory (partners read from
+// global memory as well: 95 us instead of __ROPE_IMAGE__ us at B8 H8 n12288 d64 with axes
+// 24, 24, 16).
 // grid (blocks over tokens x pieces, batch x head groups), block 256.
 template <typename T, int D, int W, bool ADJ>
 __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
   constexpr int N = 16 / sizeof(T), kPieces = D / N;  // a row's pieces lie in one warp
+  constexpr int kTok = 256 / kPieces;
   using P = Piece<N, W, ADJ>;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t tok = id / kPieces;
-  const int dim0 = (int)(id % kPieces) * N;
+  __shared__ float ct[ADJ ? 1 : kTok * D / 2], st[ADJ ? 1 : kTok * D / 2];
+  __shared__ uint4 swap[ADJ ? 1 : kRopeHeads][256];
+  const int64_t tok0 = (int64_t)blockIdx.x * kTok;
+  const int tl = threadIdx.x / kPieces, dim0 = threadIdx.x % kPieces * N;
+  const int64_t tok = tok0 + tl;
   const bool in = tok < A.n;
+  const int pairs = A.rot.pairs;
   P piece;
   piece.place(A.rot, dim0);
   for (int64_t bg = blockIdx.y; bg < (int64_t)A.B * A.head_groups; bg += gridDim.y) {
     const int b = (int)(bg / A.head_groups), h0 = (int)(bg % A.head_groups) * A.heads_per;
     const int h1 = min(h0 + A.heads_per, A.H);
-    const T* xp = x + b * A.xs[0] + (in ? tok : 0) * A.xs[2];
+    const T* xp = x + b * A.xs[0] + (in ? tok : 0) * A.xs[2] + dim0;
     T* op = out + b * A.os[0] + tok * A.os[2] + dim0;
+    const int32_t* pos = A.pos + b * A.pos_batch;
     float c[P::kPairs], s[P::kPairs];
+    if constexpr (!ADJ) {
+      __syncthreads();  // the angles of the batch before have been taken
+      const int toks = (int)min((int64_t)kTok, A.n - tok0);
+      for (int i = threadIdx.x; i < toks * pairs; i += 256) {
+        const int p = i % pairs;
+        rot_angle(pos[rot_axis(A.rot, p) * A.pos_axis + tok0 + i / pairs], A.freqs[p], &ct[i], &st[i]);
+      }
+      __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < P::kPairs; ++i) {
       c[i] = 1.f;
       s[i] = 0.f;
       if (in && (piece.turned >> i & 1)) {
         const int p = piece.pair_of(i);
-        rot_angle(A.pos[rot_axis(A.rot, p) * A.pos_axis + b * A.pos_batch + tok], A.freqs[p], &c[i],
-                  &s[i]);
+        if constexpr (ADJ) {
+          rot_angle(pos[rot_axis(A.rot, p) * A.pos_axis + tok], A.freqs[p], &c[i], &s[i]);
+        } else {
+          c[i] = ct[tl * pairs + p];
+          s[i] = st[tl * pairs + p];
+        }
         s[i] *= A.sign * piece.sign_of(i);
       }
     }
-    // heads in batches, all of a batch loaded before the first is stored; x and
-    // out may be the same rows, so a warp's partners are read before any lane
-    // writes
+    // heads in batches, all of a batch loaded before the first is stored (x and
+    // out may be the same rows)
     for (int h = h0; h < h1; h += kRopeHeads) {
       uint4 u[kRopeHeads];
-      float y[kRopeHeads][N];
 #pragma unroll
       for (int k = 0; k < kRopeHeads; ++k)
-        if (h + k < h1) {
-          const T* row = xp + (h + k) * A.xs[1];
-          u[k] = *reinterpret_cast<const uint4*>(row + dim0);
-          if constexpr (!ADJ) {
+        if (h + k < h1) u[k] = *reinterpret_cast<const uint4*>(xp + (h + k) * A.xs[1]);
+      if constexpr (!ADJ) {
 #pragma unroll
-            for (int r = 0; r < P::kRuns; ++r) load_w<T, W>(row + piece.other[r], &y[k][r * W]);
-          }
-        }
-      __syncwarp();
+        for (int k = 0; k < kRopeHeads; ++k) swap[k][threadIdx.x] = u[k];
+        __syncwarp();
+      }
 #pragma unroll
       for (int k = 0; k < kRopeHeads; ++k)
         if (h + k < h1 && in) {
-          float f[N];
+          float f[N], y[N];
           Vec16<T>::unpack(u[k], f);
-          piece.turn(f, y[k], c, s);
+          if constexpr (!ADJ) {
+            const T* row = reinterpret_cast<const T*>(&swap[k][tl * kPieces]);
+#pragma unroll
+            for (int r = 0; r < P::kRuns; ++r) load_w<T, W>(row + piece.other[r], &y[r * W]);
+          }
+          piece.turn(f, y, c, s);
           *reinterpret_cast<uint4*>(op + (h + k) * A.os[1]) = pack16<T>(f);
         }
+      if constexpr (!ADJ) __syncwarp();
     }
   }
 }

@@ -132,17 +132,14 @@ def append(cache, rows, v, page_table, seq_len, n_valid=None, x=None):
 def read(cache, page_table, b, h, count):
     """The first `count` cached tokens of sequence b: keys' rows, values, 1/||x||, in float64."""
     P = cache["k"].shape[2]
-    k, v, kinv = [], [], []
-    for p in range(count):
-        page, slot = int(page_table[b, p // P]), p % P
-        kr, vr = cache["k"][page, h, slot].double(), _v_row(cache, page, h, slot).double()
-        if cache["k_scale"] is not None:
-            kr = kr * float(cache["k_scale"][page, h])
-            vr = vr * float(cache["v_scale"][page, h])
-        k.append(kr)
-        v.append(vr)
-        kinv.append(float(cache["key_inv_norm"][page, h, slot]))
-    return torch.stack(k), torch.stack(v), torch.tensor(kinv, dtype=torch.float64)
+    p = torch.arange(count)
+    page, slot = page_table[b].long()[p // P], p % P
+    k = cache["k"][page, h, slot].double()
+    v = cache["v"][page, h, slot // 16, :, slot % 16].double()
+    if cache["k_scale"] is not None:
+        k = k * cache["k_scale"][page, h].double()[:, None]
+        v = v * cache["v_scale"][page, h].double()[:, None]
+    return k, v, cache["key_inv_norm"][page, h, slot].double()
 
 
 def attend(cache, x, page_table, seq_len, n_valid=None):

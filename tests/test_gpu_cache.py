@@ -12,6 +12,9 @@ Tolerances. A rounding to bf16 is off by at most 2^-8 of the value, one to fp32 
   (rows are N(0, 1), d >= 64) that is at most 2 d 2^-24 + 2^-21 < 2^-15 for d = 128. Weights are
   off by twice that, 2^-14, 2^-20 for the exponential, and the sums of up to n terms of one sign
   by less than 2^-14 for the lengths here; the output by 2^-13 of sum p |v| and its own rounding.
+  Over an int8 cache weights are f16, held 2^14 times larger: below 2^-14 their steps are 2^-24, so a
+  weight is off by half of it over 2^14, 2^-39 of the row's largest weight, which is at most the sum:
+  the output by 2^-39 sum |v| besides.
 * lse: the logits' 2^-15, 2^-14 for the sum, and the rounding of the result.
 """
 import math
@@ -366,6 +369,37 @@ def test_attend_long_and_many(B, H, d, page, lens, n, int8):
     check_attend(to_gpu(ref), ref, table, q, lens)
 
 
+def random_cache(B, H, d, page, int8, lens, n, seed=3):
+    """A cache filled at random (as tensors, quickly), its table, and n rows of x."""
+    total = max(lens) + n
+    per_seq = total // page + 1
+    pages = B * per_seq + 1
+    c = {"k": randn(pages, H, page, d, seed=seed), "v": randn(pages, H, page // 16, d, 16, seed=seed + 1),
+         "k_scale": None, "v_scale": None}
+    c["key_inv_norm"] = 1.0 / c["k"].norm(dim=-1)
+    for name in ("k", "v"):
+        if int8:
+            c[name] = (c[name] * 25).round().clamp(-127, 127).to(torch.int8)
+            c[name + "_scale"] = 2.0 ** torch.randint(-6, -3, (pages, H)).float()
+        else:
+            c[name] = c[name].bfloat16()
+    return c, table_of(B, per_seq, pages, seed), randn(B, H, n, d, seed=seed + 2).bfloat16()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("B,H,d,page,lens,n", [
+    (3, 16, 128, 64, [3000, 2500, 3100], 1),              # the ring turns over many times in a block
+    (4, 16, 64, 32, [9000, 11, 7000, 8999], 3),
+    (64, 16, 64, 16, [(53 * i) % 130 for i in range(64)], 2),  # segments of one to a few units
+    (64, 16, 128, 128, [(29 * i) % 200 for i in range(64)], 9),
+    (2, 2, 64, 64, [40000, 33333], 1),
+])
+def test_attend_work_of_every_shape(B, H, d, page, lens, n, int8):
+    ref, table, q = random_cache(B, H, d, page, int8, lens, n)
+    valid = None if n == 1 else [(n + b) % (n + 1) for b in range(B)]
+    check_attend(to_gpu(ref), ref, table, q, lens, valid)
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_attend_values_of_different_sizes(int8):
     """Pages whose scales differ by 2^12 and 2^24."""
@@ -393,7 +427,8 @@ def test_attend_sharp_and_flat_rows():
         out, lse = lb.lsh_cache_attend(gpu, q.cuda(), table.cuda(), torch.tensor([L]).int().cuda())
         ro, rl, mag = oc.attend(ref, q, table, [L])
         # the derived bound with ||x|| = 60 * 2 sqrt(d): 60 times the logits' share
-        near(out, ro, ro.abs() * 2.0 ** -8 + mag * 60 * 2.0 ** -13, "out")
+        small = 2.0 ** -39 * oc.read(ref, table, 0, 0, L + 2)[1].abs().sum(0) if int8 else 0.0
+        near(out, ro, ro.abs() * 2.0 ** -8 + mag * 60 * 2.0 ** -13 + small, "out")
         near(lse, rl, 60 * 2.0 ** -13 + rl.abs() * 2.0 ** -23, "lse")
 
 
