@@ -166,38 +166,38 @@ lsh_status launch_append(const AppendArgs& A, bool i8, cudaStream_t st) {
   }
 }
 
-// Workspace of the cached attention: for every block a record, and two partial
-// results of eight rows.
+// Workspace of the cached attention: for every segment a record, and for every
+// computing warp two partial results of eight rows.
 struct AttendLayout {
-  int blocks;
+  int blocks, groups;
+  int64_t segments;
   size_t ml, part, total;
 };
 
-AttendLayout attend_layout(int d) {
+AttendLayout attend_layout(const lsh_cache_desc& c, const lsh_cache_rows& r) {
   AttendLayout L;
-  L.blocks = sm_count() * (d == 64 ? AttCfg<64, false>::kBlocks : AttCfg<128, false>::kBlocks);
-  const size_t rows = (size_t)L.blocks * 2 * kAttRows;
+  L.blocks = sm_count();
+  L.groups = (r.n + kAttRows - 1) / kAttRows;
+  L.segments = (int64_t)r.batch * c.heads * L.groups;
+  const int warps = c.d == 64 ? AttCfg<64, false>::kWarps : AttCfg<128, false>::kWarps;
+  const size_t rows = (size_t)L.blocks * warps * 2 * kAttRows;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  L.ml = up((size_t)L.blocks * 32);
+  L.ml = up((size_t)L.segments * sizeof(int2));
   L.part = L.ml + up(rows * 2 * sizeof(float));
-  L.total = L.part + up(rows * d * sizeof(float));
+  L.total = L.part + up(rows * c.d * sizeof(float));
   return L;
 }
 
 template <int D, bool I8>
-lsh_status launch_attend(const AttendArgs& A, cudaStream_t st) {
+lsh_status launch_attend(const AttendArgs& A, const AttendLayout& L, cudaStream_t st) {
   using Cfg = AttCfg<D, I8>;
-  static_assert(Cfg::kStages >= kAttWarps && Cfg::kStages <= 16 && Cfg::kStages % 2 == 0, "ring");
-  // those of the two batches looked up and of the ring: a joined segment has two
-  // units at least
-  static_assert(kSegRing > Cfg::kStages / 2 + 3, "segments in flight");
+  static_assert(Cfg::kWarps * Cfg::kDepth <= 32, "barriers");
   static_assert(sizeof(UnitMeta) <= 128 && Cfg::kStage % 16 == 0, "stage header");
-  static_assert(128 * 4 + 2 * 16 * 8 + kSegRing * sizeof(SegInfo) <= 2048, "fixed part");
+  static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
   auto kern = k_cache_attend<D, I8>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, Cfg::kSmem, &done)) return LSH_ERR_CUDA;
-  const unsigned blocks = (unsigned)attend_layout(D).blocks;
-  kern<<<blocks, kAttThreads, Cfg::kSmem, st>>>(A);
+  kern<<<L.blocks, Cfg::kThreads, Cfg::kSmem, st>>>(A);
   if (cudaGetLastError() != cudaSuccess) return LSH_ERR_CUDA;
   // a table that holds one unit at most leaves nothing to join
   if ((int64_t)A.S.max_pages * A.C.P <= Cfg::kTok) return LSH_OK;
@@ -205,8 +205,8 @@ lsh_status launch_attend(const AttendArgs& A, cudaStream_t st) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks, (unsigned)std::min(A.S.n, kAttRows));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)L.segments, (unsigned)std::min(A.S.n, kAttRows));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -333,7 +333,9 @@ lsh_status lsh_cache_attend_workspace_size(const lsh_cache_desc* desc, const lsh
   lsh_status s = check_cache(desc, nullptr, rows, nullptr, nullptr, nullptr, nullptr, nullptr);
   if (s != LSH_OK) return s;
   if (!bytes) return LSH_ERR_INVALID_ARG;
-  *bytes = attend_layout(desc->d).total;
+  const AttendLayout L = attend_layout(*desc, *rows);
+  if (L.segments > INT32_MAX) return LSH_ERR_UNSUPPORTED;
+  *bytes = L.total;
   return LSH_OK;
 }
 
@@ -349,7 +351,8 @@ lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
   if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->out_stride, 2) ||
       !rows_apart(rows->out_stride, A.S.B, A.C.H, A.S.n, A.C.d))
     return LSH_ERR_INVALID_ARG;
-  const AttendLayout L = attend_layout(A.C.d);
+  const AttendLayout L = attend_layout(*desc, *rows);
+  if (L.segments > INT32_MAX) return LSH_ERR_UNSUPPORTED;
   if (!ws || ((uintptr_t)ws & 255) != 0 || ws_bytes < L.total) return LSH_ERR_WORKSPACE;
   A.x = static_cast<const __nv_bfloat16*>(x);
   A.out = static_cast<__nv_bfloat16*>(out);
@@ -359,13 +362,14 @@ lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
     A.os[i] = rows->out_stride[i];
   }
   unsigned char* w = static_cast<unsigned char*>(ws);
-  A.rec = reinterpret_cast<int*>(w);
+  A.groups = L.groups;
+  A.rec = reinterpret_cast<int2*>(w);
   A.part_ml = reinterpret_cast<float*>(w + L.ml);
   A.part = reinterpret_cast<float*>(w + L.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool i8 = desc->format == LSH_CACHE_I8;
-  if (A.C.d == 64) return i8 ? launch_attend<64, true>(A, st) : launch_attend<64, false>(A, st);
-  return i8 ? launch_attend<128, true>(A, st) : launch_attend<128, false>(A, st);
+  if (A.C.d == 64) return i8 ? launch_attend<64, true>(A, L, st) : launch_attend<64, false>(A, L, st);
+  return i8 ? launch_attend<128, true>(A, L, st) : launch_attend<128, false>(A, L, st);
 }
 
 }  // extern "C"
