@@ -14,16 +14,16 @@
 // share leaves partial sums in the workspace, which k_cache_combine joins in a
 // fixed order.
 //
-// Block (persistent, one an SM). Two warps copy, each for half of the computing
-// warps: four lanes walk a warp's run, look the pages of its next unit up and
-// fill its own ring of shared-memory stages by bulk copies.
+// Block (persistent, one an SM). Four warps copy, each for a quarter of the
+// computing warps: four lanes walk a warp's run, look the pages of its next unit
+// up and fill its own ring of shared-memory stages by bulk copies.
 //
 // S = Q K^T and O += P V are warp products (m16n8k16): eight rows do not fill a
 // tcgen05 tile, and DRAM allows ten times the tensor work. A contraction's index
-// may be permuted at will as long as both operands agree, so a lane takes the
-// dimensions of K (and the tokens of V, whose groups lie dimension by dimension
-// in the cache) that are consecutive in memory, by 16 bytes, and feeds them to
-// the products as they are: no transposes, no shuffles. In bf16 the 16 rows of P
+// may be permuted at will as long as both operands agree, so a lane takes
+// dimensions of K (16 bytes) and tokens of V (four of a group of 16, which lies
+// dimension by dimension in the cache) that are consecutive in memory, and feeds
+// them to the products as they are: no transposes, no shuffles. In bf16 the 16 rows of P
 // hold the weights of eight as high and low parts, 2^-17 together, so that P V
 // loses nothing against fp32 weights.
 //
@@ -67,7 +67,7 @@ struct UnitMeta {
   int flags, slot;      // kFirst ...; slot of a partial result
   int n;                // the unit's number in the warp's run
   uint32_t ok;          // bit s: tokens 16 s .. of the unit are there
-  float ks[4], vs[4];   // their scales (int8)
+  float ks[4], lv[4];   // int8: scales of k, log2 of those of v
 };
 // of the warp's units of a segment: the first, the last, all; nothing follows
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kEnd = 8;
@@ -77,18 +77,15 @@ struct AttCfg {
   static constexpr int E = I8 ? 1 : 2;
   static constexpr int kTok = 4096 / (D * E);       // tokens of a unit
   static constexpr int kGroups = kTok / 16;
-  static constexpr int kLane = kTok / 4;            // tokens of a lane
-  // groups of v are set apart so that the pieces that lanes read together lie in
-  // different banks
-  static constexpr int kVGroup = 16 * D * E + (kGroups == 4 ? 32 : kGroups == 2 ? 64 : 0);
-  static constexpr int kV = 4096, kNorm = kV + kGroups * kVGroup;  // offsets in a stage
+  static constexpr int kV = 4096, kNorm = 8192;     // offsets in a stage
   static constexpr int kMeta = kNorm + kTok * 4;
   static constexpr int kStage = kMeta + 128;
   // computing warps and each one's stages: what registers (128 a thread for d 64,
   // 168 for d 128) and shared memory have room for
   static constexpr int kWarps = D == 64 ? 12 : 8;
   static constexpr int kDepth = D == 64 ? 2 : 3;
-  static constexpr int kThreads = 32 * (kWarps + 2);
+  static constexpr int kCopy = 4;                   // copying warps
+  static constexpr int kThreads = 32 * (kWarps + kCopy);
   static constexpr int kSmem = 512 + kWarps * kDepth * kStage;
 };
 
@@ -167,13 +164,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Copying warp `pw`: lanes 4 q .. 4 q + 3 serve computing warp pw * kWarps / 2 + q,
+// Copying warp `pw`: lanes 4 q .. 4 q + 3 serve computing warp pw kWarps / 4 + q,
 // lane 4 q + s the tokens 16 s .. of its units. The lane groups go their own ways.
 template <int D, bool I8>
 __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64_t* full,
                               uint64_t* empty, int pw) {
   using Cfg = AttCfg<D, I8>;
-  constexpr int NG = Cfg::kGroups, kServe = Cfg::kWarps / 2;
+  constexpr int NG = Cfg::kGroups, kServe = Cfg::kWarps / Cfg::kCopy;
   const CacheView& C = A.C;
   const SeqTables& S = A.S;
   const int lane = threadIdx.x & 31, q = lane >> 2, sl = lane & 3;
@@ -333,7 +330,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
       const uint32_t ok = (__ballot_sync(mine, cur.id >= 0) >> (4 * q)) & 15;
       if (I8) {
         mt->ks[sl] = ks;
-        mt->vs[sl] = vs;
+        mt->lv[sl] = cur.id >= 0 ? log2f(vs) : -INFINITY;
       }
       if (sl == 0) {
         mt->b = cur.b;
@@ -362,9 +359,9 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
                                take * 16 * D * Cfg::E, &full[slot]);
           sm100::bulk_copy_g2s(sp + Cfg::kNorm + sl * 64, C.kinv + (hs << pshift) + ps, take * 64,
                                &full[slot]);
+          sm100::bulk_copy_g2s(sp + Cfg::kV + sl * 16 * D * Cfg::E, static_cast<char*>(C.v) + from,
+                               take * 16 * D * Cfg::E, &full[slot]);
         }
-        sm100::bulk_copy_g2s(sp + Cfg::kV + sl * Cfg::kVGroup, static_cast<char*>(C.v) + from,
-                             16 * D * Cfg::E, &full[slot]);
       } else if (sl < NG && !(cur.flags & kEnd) && cur.t0 + 16 * sl < cur.len + cur.q0 + cur.rows) {
         cache_error(C);  // a bad page
       }
@@ -421,11 +418,9 @@ template <int D, bool I8>
 __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(AttendArgs A) {
   using Cfg = AttCfg<D, I8>;
   using T = std::conditional_t<I8, __half, bf16>;
-  constexpr int NG = Cfg::kGroups, TL = Cfg::kLane;
+  constexpr int NG = Cfg::kGroups;
   constexpr int kSteps = D / 16;  // 16-wide steps of Q K^T
   constexpr int kN = D / 8;       // 8-wide column tiles of P V
-  constexpr int kJ = TL / 2;      // 8-token tiles of S
-  constexpr int kP = TL / 4;      // 16-token steps of P V
   extern __shared__ __align__(16) unsigned char smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + 32;
@@ -453,7 +448,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   float o[kN][4];
   float m = -INFINITY, l = 0.f;      // the row's reference; sum of this lane's weights
   float qscale = 1.f, qbias = 0.f;   // int8: x is qa * qscale / 2^10; -128 sum qa / 2^24
-  float vref = 0.f;                  // int8: o counts in units of the scale vref
+  float vref = -INFINITY;            // int8: o counts in units of the scale 2^vref
   int st = 0;
   uint32_t ph = 0;
 
@@ -523,74 +518,75 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
         for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
       m = -INFINITY;
       l = 0.f;
-      vref = 0.f;
+      vref = -INFINITY;
     }
     if (__any_sync(~0u, !sm100::mbar_wait(&full[slot], ph))) {
       late = true;
       break;
     }
 
-    // S: column c of tile j is token TL (c / 2) + 2 j + c % 2, so that this lane
-    // holds tokens TL t .. of row g: tokens 2 j and 2 j + 1 of its own in tile j
-    float p[TL];
+    // S, two tiles of eight tokens for each group of 16: column c of tile e is the
+    // group's token 4 (c / 2) + 2 e + c % 2, so that this lane holds its tokens
+    // 4 t .. 4 t + 3 for row g
+    float p[NG][4];
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      float s[4] = {qbias, qbias, 0.f, 0.f};
-      const unsigned char* kp = sp + (TL * (g >> 1) + 2 * j + (g & 1)) * D * Cfg::E + 16 * t;
+    for (int j = 0; j < NG; ++j)
 #pragma unroll
-      for (int i = 0; i < D * Cfg::E / 64; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4*>(kp + 64 * i);
-        if constexpr (I8) {
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int e = 0; e < 2; ++e) {
+        float s[4] = {qbias, qbias, 0.f, 0.f};
+        const unsigned char* kp = sp + (16 * j + 4 * (g >> 1) + 2 * e + (g & 1)) * D * Cfg::E + 16 * t;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t b0, b1;
-            i8_to_sub(w[k], &b0, &b1);
-            const int a = 2 * (4 * i + k);
-            mma_16816(s, qa[a], 0u, qa[a + 1], 0u, b0, b1, T());
+        for (int i = 0; i < D * Cfg::E / 64; ++i) {
+          const uint4 u = *reinterpret_cast<const uint4*>(kp + 64 * i);
+          if constexpr (I8) {
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t b0, b1;
+              i8_to_sub(w[k], &b0, &b1);
+              const int a = 2 * (4 * i + k);
+              mma_16816(s, qa[a], 0u, qa[a + 1], 0u, b0, b1, T());
+            }
+          } else {
+            mma_16816(s, qa[4 * i], 0u, qa[4 * i + 1], 0u, u.x, u.y, T());
+            mma_16816(s, qa[4 * i + 2], 0u, qa[4 * i + 3], 0u, u.z, u.w, T());
           }
-        } else {
-          mma_16816(s, qa[4 * i], 0u, qa[4 * i + 1], 0u, u.x, u.y, T());
-          mma_16816(s, qa[4 * i + 2], 0u, qa[4 * i + 3], 0u, u.z, u.w, T());
         }
+        p[j][2 * e] = s[0];
+        p[j][2 * e + 1] = s[1];
       }
-      p[2 * j] = s[0];
-      p[2 * j + 1] = s[1];
-    }
-    const int tok0 = mt->t0 + TL * t;  // this lane's first token
-    const int grp = TL * t / 16;       // and its group
     const uint32_t ok = mt->ok;
-    const bool there = ok >> grp & 1;
-    float f = cs;
-    if constexpr (I8) f *= mt->ks[grp] * 1024.f * qscale;
+    const int row0 = mt->len + mt->q0;  // position of row 0
+    float top = -INFINITY, vtop = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < TL / 4; ++j) {
-      const float4 kn = *reinterpret_cast<const float4*>(sp + Cfg::kNorm + (TL * t + 4 * j) * 4);
-      p[4 * j] *= kn.x * f;
-      p[4 * j + 1] *= kn.y * f;
-      p[4 * j + 2] *= kn.z * f;
-      p[4 * j + 3] *= kn.w * f;
+    for (int j = 0; j < NG; ++j) {
+      const float4 kn = *reinterpret_cast<const float4*>(sp + Cfg::kNorm + (16 * j + 4 * t) * 4);
+      float f = cs;
+      if constexpr (I8) {
+        f *= mt->ks[j] * 1024.f * qscale;
+        vtop = fmaxf(vtop, mt->lv[j]);
+      }
+      p[j][0] *= kn.x * f;
+      p[j][1] *= kn.y * f;
+      p[j][2] *= kn.z * f;
+      p[j][3] *= kn.w * f;
     }
     // units with tokens that some row must not see, or that are not there
-    const int row0 = mt->len + mt->q0;  // position of row 0
     const bool tail = mt->t0 + Cfg::kTok > row0 || ok != (1u << NG) - 1;
     if (tail) {
-      const int self = row0 + g - tok0;  // row g's own token
 #pragma unroll
-      for (int k = 0; k < TL; ++k)
-        p[k] = k > self || !there ? -INFINITY : k == self ? kSelfLogit * kLog2e : p[k];
-    }
-    float top = p[0];
+      for (int j = 0; j < NG; ++j) {
+        const int self = row0 + g - (mt->t0 + 16 * j + 4 * t);  // row g's own token
+        const bool there = ok >> j & 1;
 #pragma unroll
-    for (int k = 1; k < TL; ++k) top = fmaxf(top, p[k]);
-    float vs = 1.f, vm = 0.f;
-    if constexpr (I8) {
-      // the unit's largest scale: the lanes of a row hold all its groups
-      vs = there ? mt->vs[grp] : 0.f;
-      vm = fmaxf(vs, __shfl_xor_sync(~0u, vs, 1));
-      vm = fmaxf(vm, __shfl_xor_sync(~0u, vm, 2));
+        for (int k = 0; k < 4; ++k)
+          p[j][k] = k > self || !there ? -INFINITY : k == self ? kSelfLogit * kLog2e : p[j][k];
+      }
     }
-    if (__any_sync(~0u, top > m + kOver || vm > vref)) {
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+      top = fmaxf(top, fmaxf(fmaxf(p[j][0], p[j][1]), fmaxf(p[j][2], p[j][3])));
+    if (__any_sync(~0u, top > m + kOver || vtop > vref)) {
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
       float corr = 1.f;
@@ -599,111 +595,104 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
         m = top;
         l *= corr;
       }
-      if (I8 && vm > vref) {
-        corr *= vref / vm;
-        vref = vm;
+      if (I8 && vtop > vref) {
+        corr *= ex2(vref - vtop);
+        vref = vtop;
       }
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] *= corr;
     }
-    float ref = m == -INFINITY ? 0.f : m - kUp, back = 1.f;
-    if constexpr (I8) {
-      // weights carry the ratio of their group's scale to vref (2^-64 is nothing
-      // beside a step of vref, and leaves its reciprocal in range)
-      const float ratio = there ? fmaxf(vs / vref, 0x1p-64f) : 1.f;
-      ref -= __log2f(ratio);
-      back = 1.f / ratio;
-    }
-    float sum = 0.f;
+    // P as A operand: the step of group j is its two tiles; bf16: high and low part
+    uint32_t a[NG][2], al[NG][2];
+    const float ref0 = m == -INFINITY ? 0.f : m - kUp;
 #pragma unroll
-    for (int k = 0; k < TL; ++k) {
-      p[k] = ex2(p[k] - ref);
-      sum += p[k];
-    }
-    l = I8 ? fmaf(sum, back, l) : l + sum;
-    // P as A operand: step s is tiles 2 s and 2 s + 1; bf16: high and low part
-    uint32_t a[kJ], al[kJ];
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) {
+    for (int j = 0; j < NG; ++j) {
+      float ref = ref0, back = 1.f;
       if constexpr (I8) {
-        a[j] = pack_h2(p[2 * j], p[2 * j + 1]);
-        al[j] = 0u;
-      } else {
-        split2(p[2 * j], p[2 * j + 1], &a[j], &al[j]);
+        // weights carry the ratio of their group's scale to 2^vref (2^-64 is nothing
+        // beside a step of it, and leaves its reciprocal in range)
+        const float lr = ok >> j & 1 ? fmaxf(mt->lv[j] - vref, -64.f) : 0.f;
+        ref -= lr;
+        back = ex2(-lr);
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        p[j][k] = ex2(p[j][k] - ref);
+        sum += p[j][k];
+      }
+      l = I8 ? fmaf(sum, back, l) : l + sum;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (I8) {
+          a[j][e] = pack_h2(p[j][2 * e], p[j][2 * e + 1]);
+          al[j][e] = 0u;
+        } else {
+          split2(p[j][2 * e], p[j][2 * e + 1], &a[j][e], &al[j][e]);
+        }
       }
     }
-    // v: this lane's tokens of a dimension are 16 or 8 bytes
-    constexpr int kW = TL * Cfg::E / 4;  // words
-    const unsigned char* vp = sp + Cfg::kV + grp * Cfg::kVGroup + (g * 16 + TL * t % 16) * Cfg::E;
-    auto load_v = [&](int i, uint32_t (&w)[kW]) {
-      if constexpr (kW == 4) {
-        const uint4 u = *reinterpret_cast<const uint4*>(vp + i * 128 * Cfg::E);
-        w[0] = u.x;
-        w[1] = u.y;
-        w[2] = u.z;
-        w[3] = u.w;
+    // v: four tokens of a dimension, 4 or 8 bytes
+    const unsigned char* vp = sp + Cfg::kV + (g * 16 + 4 * t) * Cfg::E;
+    auto load_v = [&](int j, int i, uint32_t* b0, uint32_t* b1) {
+      const unsigned char* at = vp + j * 16 * D * Cfg::E + i * 128 * Cfg::E;
+      if constexpr (I8) {
+        i8_to_f16(*reinterpret_cast<const uint32_t*>(at), b0, b1);
       } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(vp + i * 128 * Cfg::E);
-        w[0] = u.x;
-        w[1] = u.y;
+        const uint2 u = *reinterpret_cast<const uint2*>(at);
+        *b0 = u.x;
+        *b1 = u.y;
       }
     };
     if (I8 || !tail) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        uint32_t w[kW];
-        load_v(i, w);
+      for (int i = 0; i < kN; ++i)
 #pragma unroll
-        for (int k = 0; k < kP; ++k) {
+        for (int j = 0; j < NG; ++j) {
           uint32_t b0, b1;
-          if constexpr (I8) {
-            i8_to_f16(w[k], &b0, &b1);
-          } else {
-            b0 = w[2 * k];
-            b1 = w[2 * k + 1];
-          }
-          mma_16816(o[i], a[2 * k], al[2 * k], a[2 * k + 1], al[2 * k + 1], b0, b1, T());
+          load_v(j, i, &b0, &b1);
+          mma_16816(o[i], a[j][0], al[j][0], a[j][1], al[j][1], b0, b1, T());
         }
-      }
     } else if constexpr (!I8) {
       // bf16 values that some row must not see: slots behind the last row, and
       // groups that are not there, hold anything, and a later row's value may be
       // infinite; 0 times it is NaN. The former are cleared; where one of the
       // latter is not finite, the tokens go one by one and each row takes its own.
-      const int count = there ? row0 + mt->rows - tok0 : 0;  // of this lane's, those that count
-      uint32_t keep[kW], odd = 0;
+      uint32_t k0[NG], k1[NG], odd = 0;
 #pragma unroll
-      for (int k = 0; k < kW; ++k)
-        keep[k] = count >= 2 * k + 2 ? ~0u : count == 2 * k + 1 ? 0xffffu : 0u;
+      for (int j = 0; j < NG; ++j) {
+        // of this lane's tokens, those that count
+        const int count = ok >> j & 1 ? row0 + mt->rows - (mt->t0 + 16 * j + 4 * t) : 0;
+        k0[j] = count >= 2 ? ~0u : count == 1 ? 0xffffu : 0u;
+        k1[j] = count >= 4 ? ~0u : count == 3 ? 0xffffu : 0u;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        uint32_t w[kW];
-        load_v(i, w);
-#pragma unroll
-        for (int k = 0; k < kW; ++k)
-          odd |= (uint32_t)((w[k] & keep[k] & 0x7f80u) == 0x7f80u) |
-                 (uint32_t)((w[k] & keep[k] & 0x7f800000u) == 0x7f800000u);
+        for (int i = 0; i < kN; ++i) {
+          uint32_t b0, b1;
+          load_v(j, i, &b0, &b1);
+          b0 &= k0[j];
+          b1 &= k1[j];
+          odd |= (uint32_t)((b0 & 0x7f80u) == 0x7f80u) | (uint32_t)((b0 & 0x7f800000u) == 0x7f800000u) |
+                 (uint32_t)((b1 & 0x7f80u) == 0x7f80u) | (uint32_t)((b1 & 0x7f800000u) == 0x7f800000u);
+        }
       }
       const bool apart = __any_sync(~0u, odd);
       for (int tk = 0; tk < (apart ? Cfg::kTok : 1); ++tk) {
-        uint32_t e[kW];
-#pragma unroll
-        for (int k = 0; k < kW; ++k)
-          e[k] = !apart ? keep[k]
-                 : tk / TL == t && tk % TL / 2 == k ? keep[k] & (tk & 1 ? 0xffff0000u : 0xffffu)
-                                                    : 0u;
         const bool sees = !apart || mt->t0 + tk <= row0 + g;
+        const uint32_t half = tk & 1 ? 0xffff0000u : 0xffffu;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          uint32_t w[kW];
-          load_v(i, w);
           float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int k = 0; k < kP; ++k)
-            mma_16816(d, a[2 * k], al[2 * k], a[2 * k + 1], al[2 * k + 1], w[2 * k] & e[2 * k],
-                      w[2 * k + 1] & e[2 * k + 1], T());
+          for (int j = 0; j < NG; ++j) {
+            uint32_t b0, b1;
+            load_v(j, i, &b0, &b1);
+            const bool here = tk / 16 == j && tk % 16 / 4 == t;
+            b0 &= !apart ? k0[j] : here && !(tk & 2) ? half & k0[j] : 0u;
+            b1 &= !apart ? k1[j] : here && (tk & 2) ? half & k1[j] : 0u;
+            mma_16816(d, a[j][0], al[j][0], a[j][1], al[j][1], b0, b1, T());
+          }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (sees) o[i][k] += d[k];
@@ -716,7 +705,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       L += __shfl_xor_sync(~0u, L, 2);
       L *= kDown;
       if (g < mt->rows) {
-        float f1 = I8 ? vref * kDown : 1.f;
+        float f1 = I8 && vref > -INFINITY ? exp2f(vref) * kDown : 1.f;
         if (flags & kWhole) {
           f1 *= L == 0.f ? 0.f : 1.f / L;
           bf16* op = A.out + mt->b * A.os[0] + mt->h * A.os[1] + (int64_t)(mt->q0 + g) * A.os[2] + 2 * t;
