@@ -152,6 +152,12 @@ __device__ __forceinline__ int64_t att_units(int H, int len, int nv, int* groups
   return (int64_t)H * *groups * *units;
 }
 
+// a / b of numbers that are not negative, by 32 bits where they fit.
+__device__ __forceinline__ int64_t udiv(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -193,15 +199,20 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) N += __shfl_xor_sync(kAll, N, o);
-  // runs of two units at least; neighbouring runs lie in different blocks
-  const int64_t G = min((int64_t)gridDim.x * Cfg::kWarps, (N + 1) / 2);
-  const int64_t run = (int64_t)wk * gridDim.x + blockIdx.x;
+  // G runs of `each` units, the first `more` of them one longer; neighbouring runs
+  // lie in different blocks
+  const int64_t G = max((int64_t)1, min((int64_t)gridDim.x * Cfg::kWarps, N));
+  const int run = wk * (int)gridDim.x + (int)blockIdx.x;
+  const int64_t each = udiv(N, G), more = N - each * G;
   int64_t u = 0;
   int left = 0;  // units to come
   if (q < kServe && run < G) {
-    u = N * run / G;
-    left = (int)(N * (run + 1) / G - u);
+    u = run * each + min((int64_t)run, more);
+    left = (int)(each + (run < more));
   }
+  auto run_of = [&](int64_t x) {  // the run that unit x is in
+    return (int)(x < more * (each + 1) ? udiv(x, each + 1) : more + udiv(x - more * (each + 1), each));
+  };
 
   // the walk: unit `unit` of segment (b, h, grp); its sequence's numbers
   int b = 0, h = 0, grp = 0, unit = 0, len = 0, nv = 0;
@@ -235,9 +246,9 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
           len = l_len;
           nv = l_nv;
           att_units<Cfg::kTok>(C.H, len, nv, &groups, &units);
-          const int64_t hg = at / units;
+          const int64_t hg = udiv(at, units);
           unit = (int)(at - hg * units);
-          h = (int)(hg / groups);
+          h = (int)udiv(hg, groups);
           grp = (int)(hg - (int64_t)h * groups);
         }
       }
@@ -262,9 +273,9 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
     if (starts) {
       head = unit == 0;
       if (head && sl == 0) {
-        int2 r = make_int2((int)run, 0);
+        int2 r = make_int2(run, 0);
         if (units > left)  // it goes on in the runs behind: up to which
-          r.y = (int)(((u + units) * G - 1) / N) - (int)run + 1;
+          r.y = run_of(u + units - 1) - run + 1;
         A.rec[((int64_t)b * C.H + h) * A.groups + grp] = r;
       }
     }
@@ -427,6 +438,8 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   unsigned char* stages = smem + 512;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
+  // k_cache_combine may be brought in where there is room: it waits for our end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < Cfg::kWarps * Cfg::kDepth) {
     sm100::mbar_init(&full[threadIdx.x], 1);
     sm100::mbar_init(&empty[threadIdx.x], 1);
@@ -735,17 +748,17 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
     }
   }
   // (a wait that gave up is recorded by the copying warp, which gives up as well)
-  // k_cache_combine may be brought in
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the parts of a row that several warps of k_cache_attend have left: the
 // first one's last, then the first of each behind it, in this order whatever runs
 // when.
-// grid (segments, up to 8 rows), block 256.
+// grid (segments, up to 8 rows), block 32 .. 512: a warp for eight parts of a
+// segment or so.
 template <int D>
-__global__ void __launch_bounds__(256) k_cache_combine(AttendArgs A) {
-  constexpr int DL = D / 32, kW = 8;
+__global__ void __launch_bounds__(512) k_cache_combine(AttendArgs A) {
+  constexpr int DL = D / 32, kMost = 16, kAt = 8;
+  const int kW = blockDim.x >> 5;
   // launched while k_cache_attend still runs: wait for its end, and its writes
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int seg = blockIdx.x, row = blockIdx.y;
@@ -757,42 +770,62 @@ __global__ void __launch_bounds__(256) k_cache_combine(AttendArgs A) {
   seq_rows(A.S, A.C.P, b, &len, &nv);
   if (t >= nv) return;
   const int count = r.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float sm[kW], sl[kW], so[kW][D];
-  auto at = [&](int j) { return (((int64_t)r.x + j) * 2 + (j == 0)) * 8 + row; };
-  float M = -INFINITY;
-  for (int j = threadIdx.x; j < count; j += 256) M = fmaxf(M, A.part_ml[at(j) * 2]);
-  M = warp_max(M);
-  if (lane == 0) sm[warp] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kW; ++w) M = fmaxf(M, sm[w]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, o[DL];
+  __shared__ float sm[kMost], sl[kMost], so[kMost][D];
+  // a warp's parts, eight under way at a time, summed to the largest reference
+  float M = -INFINITY, L = 0.f, o[DL];
 #pragma unroll
   for (int k = 0; k < DL; ++k) o[k] = 0.f;
-#pragma unroll 8
-  for (int j = warp; j < count; j += kW) {
-    const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + at(j) * 2);
-    const float f = ex2(ml.x - ref);
-    L += ml.y * f;
+  for (int j0 = warp; j0 < count; j0 += kAt * kW) {
+    float2 ml[kAt];
+    float pv[kAt][DL];
 #pragma unroll
-    for (int k = 0; k < DL; ++k) o[k] += A.part[at(j) * D + lane * DL + k] * f;
+    for (int i = 0; i < kAt; ++i) {
+      const int j = j0 + i * kW;
+      const bool in = j < count;
+      const int64_t at = (((int64_t)r.x + (in ? j : 0)) * 2 + (!in || j == 0)) * 8 + row;
+      ml[i] = *reinterpret_cast<const float2*>(A.part_ml + at * 2);
+#pragma unroll
+      for (int k = 0; k < DL; ++k) pv[i][k] = A.part[at * D + lane * DL + k];
+      if (!in) ml[i] = make_float2(-INFINITY, 0.f);
+    }
+    float top = M;
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) top = fmaxf(top, ml[i].x);
+    const float ref = top == -INFINITY ? 0.f : top, was = ex2(M - ref);
+    L *= was;
+#pragma unroll
+    for (int k = 0; k < DL; ++k) o[k] *= was;
+#pragma unroll
+    for (int i = 0; i < kAt; ++i) {
+      if (j0 + i * kW >= count) break;
+      const float f = ex2(ml[i].x - ref);
+      L += ml[i].y * f;
+#pragma unroll
+      for (int k = 0; k < DL; ++k) o[k] += pv[i][k] * f;
+    }
+    M = top;
   }
-  if (lane == 0) sl[warp] = L;
+  if (lane == 0) {
+    sm[warp] = M;
+    sl[warp] = L;
+  }
 #pragma unroll
   for (int k = 0; k < DL; ++k) so[warp][lane * DL + k] = o[k];
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float sum = 0.f;
-  L = 0.f;
-#pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    L += sl[w];
-    sum += so[w][threadIdx.x];
+  for (int w = 0; w < kW; ++w) M = fmaxf(M, sm[w]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  for (int dim = threadIdx.x; dim < D; dim += blockDim.x) {
+    float sum = 0.f;
+    L = 0.f;
+    for (int w = 0; w < kW; ++w) {
+      const float f = ex2(sm[w] - ref);
+      L += sl[w] * f;
+      sum += so[w][dim] * f;
+    }
+    A.out[b * A.os[0] + h * A.os[1] + (int64_t)t * A.os[2] + dim] =
+        __float2bfloat16_rn(L == 0.f ? 0.f : sum / L);
+    if (dim == 0) A.lse[((int64_t)b * A.C.H + h) * A.S.n + t] = att_lse(M, L);
   }
-  A.out[b * A.os[0] + h * A.os[1] + (int64_t)t * A.os[2] + threadIdx.x] =
-      __float2bfloat16_rn(L == 0.f ? 0.f : sum / L);
-  if (threadIdx.x == 0) A.lse[((int64_t)b * A.C.H + h) * A.S.n + t] = att_lse(M, L);
 }
 
 }  // namespace lsh

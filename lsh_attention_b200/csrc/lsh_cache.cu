@@ -206,7 +206,9 @@ lsh_status launch_attend(const AttendArgs& A, const AttendLayout& L, cudaStream_
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)L.segments, (unsigned)std::min(A.S.n, kAttRows));
-  cfg.blockDim = dim3(256);
+  // a segment has about this many parts where it is shared at all
+  const int64_t parts = (int64_t)L.blocks * Cfg::kWarps / L.segments + 2;
+  cfg.blockDim = dim3(32u * (unsigned)std::min<int64_t>(16, std::max<int64_t>(1, parts / 8)));
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
