@@ -57,7 +57,7 @@ struct AttendArgs {
   int groups;      // segments of a (sequence, head), most
   float* part;     // [computing warps][2][8][D] unnormalised sums of split segments
   float* part_ml;  // [computing warps][2][8][2] their references (log2) and weights' sums
-  int2* rec;       // [B][H][groups]: first warp and how many share it; 0: it is whole
+  int4* rec;       // [B][H][groups]: first warp, how many share it (0: it is whole), rows
 };
 
 // A ring stage's header, written by the copying warp.
@@ -273,7 +273,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
     if (starts) {
       head = unit == 0;
       if (head && sl == 0) {
-        int2 r = make_int2(run, 0);
+        int4 r = make_int4(run, 0, rows, 0);
         if (units > left)  // it goes on in the runs behind: up to which
           r.y = run_of(u + units - 1) - run + 1;
         A.rec[((int64_t)b * C.H + h) * A.groups + grp] = r;
@@ -417,7 +417,7 @@ __device__ void att_pad_rows(const AttendArgs& A) {
     }
     const int full = (nv + kAttRows - 1) / kAttRows, none = A.groups - full;
     for (int64_t i = threadIdx.x; i < (int64_t)none * A.C.H; i += kThreads)
-      A.rec[((int64_t)b * A.C.H + i / none) * A.groups + full + i % none] = make_int2(0, 0);
+      A.rec[((int64_t)b * A.C.H + i / none) * A.groups + full + i % none] = make_int4(0, 0, 0, 0);
   }
 }
 
@@ -751,81 +751,96 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
 }
 
 // Joins the parts of a row that several warps of k_cache_attend have left: the
-// first one's last, then the first of each behind it, in this order whatever runs
-// when.
-// grid (segments, up to 8 rows), block 32 .. 512: a warp for eight parts of a
-// segment or so.
+// first one's last, then the first of each behind it. A row's 32 dimensions a
+// block, eight lanes for a part, so that all parts' loads are under way at once:
+// the time is that of two loads from L2 in turn and the launch. The order in
+// which parts are summed is that of their numbers.
+// grid (segments, up to 8 rows, D / 32), block 8 x parts or so, 32 .. 256.
 template <int D>
-__global__ void __launch_bounds__(512) k_cache_combine(AttendArgs A) {
-  constexpr int DL = D / 32, kMost = 16, kAt = 8;
-  const int kW = blockDim.x >> 5;
+__global__ void __launch_bounds__(256) k_cache_combine(AttendArgs A) {
+  constexpr int kAt = 5;  // parts of a lane that are fetched together
+  const int lane8 = threadIdx.x & 7, ps = threadIdx.x >> 3, slots = blockDim.x >> 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int seg = blockIdx.x, row = blockIdx.y, dim0 = blockIdx.z * 32;
+  __shared__ float sm[8], sl[8];
+  __shared__ __align__(16) float so[8][32];
   // launched while k_cache_attend still runs: wait for its end, and its writes
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int seg = blockIdx.x, row = blockIdx.y;
-  const int2 r = A.rec[seg];
-  const int grp = seg % A.groups, bh = seg / A.groups, t = grp * kAttRows + row;
-  const int b = bh / A.C.H, h = bh - b * A.C.H;
-  if (r.y == 0) return;
-  int len, nv;
-  seq_rows(A.S, A.C.P, b, &len, &nv);
-  if (t >= nv) return;
-  const int count = r.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float sm[kMost], sl[kMost], so[kMost][D];
-  // a warp's parts, eight under way at a time, summed to the largest reference
-  float M = -INFINITY, L = 0.f, o[DL];
-#pragma unroll
-  for (int k = 0; k < DL; ++k) o[k] = 0.f;
-  for (int j0 = warp; j0 < count; j0 += kAt * kW) {
+  const int4 r = A.rec[seg];
+  const int count = r.y;
+  if (count == 0 || row >= r.z) return;
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = ps; j0 < count; j0 += kAt * slots) {
     float2 ml[kAt];
-    float pv[kAt][DL];
+    float4 pv[kAt];
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
-      const int j = j0 + i * kW;
-      const bool in = j < count;
-      const int64_t at = (((int64_t)r.x + (in ? j : 0)) * 2 + (!in || j == 0)) * 8 + row;
-      ml[i] = *reinterpret_cast<const float2*>(A.part_ml + at * 2);
-#pragma unroll
-      for (int k = 0; k < DL; ++k) pv[i][k] = A.part[at * D + lane * DL + k];
-      if (!in) ml[i] = make_float2(-INFINITY, 0.f);
+      const int j = j0 + i * slots;
+      ml[i] = make_float2(-INFINITY, 0.f);
+      pv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < count) {
+        const int64_t at = (((int64_t)r.x + j) * 2 + (j == 0)) * kAttRows + row;
+        ml[i] = *reinterpret_cast<const float2*>(A.part_ml + at * 2);
+        pv[i] = *reinterpret_cast<const float4*>(A.part + at * D + dim0 + lane8 * 4);
+      }
     }
     float top = M;
 #pragma unroll
     for (int i = 0; i < kAt; ++i) top = fmaxf(top, ml[i].x);
     const float ref = top == -INFINITY ? 0.f : top, was = ex2(M - ref);
     L *= was;
-#pragma unroll
-    for (int k = 0; k < DL; ++k) o[k] *= was;
+    o.x *= was;
+    o.y *= was;
+    o.z *= was;
+    o.w *= was;
 #pragma unroll
     for (int i = 0; i < kAt; ++i) {
-      if (j0 + i * kW >= count) break;
       const float f = ex2(ml[i].x - ref);
-      L += ml[i].y * f;
-#pragma unroll
-      for (int k = 0; k < DL; ++k) o[k] += pv[i][k] * f;
+      L = fmaf(ml[i].y, f, L);
+      o.x = fmaf(pv[i].x, f, o.x);
+      o.y = fmaf(pv[i].y, f, o.y);
+      o.z = fmaf(pv[i].z, f, o.z);
+      o.w = fmaf(pv[i].w, f, o.w);
     }
     M = top;
   }
+#pragma unroll
+  for (int off = 8; off < 32; off <<= 1) {
+    const float M2 = __shfl_xor_sync(~0u, M, off), L2 = __shfl_xor_sync(~0u, L, off);
+    const float4 o2 = make_float4(__shfl_xor_sync(~0u, o.x, off), __shfl_xor_sync(~0u, o.y, off),
+                                  __shfl_xor_sync(~0u, o.z, off), __shfl_xor_sync(~0u, o.w, off));
+    const float top = fmaxf(M, M2), ref = top == -INFINITY ? 0.f : top;
+    const float f = ex2(M - ref), f2 = ex2(M2 - ref);
+    L = L * f + L2 * f2;
+    o.x = o.x * f + o2.x * f2;
+    o.y = o.y * f + o2.y * f2;
+    o.z = o.z * f + o2.z * f2;
+    o.w = o.w * f + o2.w * f2;
+    M = top;
+  }
+  if (lane < 8) *reinterpret_cast<float4*>(&so[warp][4 * lane]) = o;
   if (lane == 0) {
     sm[warp] = M;
     sl[warp] = L;
   }
-#pragma unroll
-  for (int k = 0; k < DL; ++k) so[warp][lane * DL + k] = o[k];
   __syncthreads();
-  for (int w = 0; w < kW; ++w) M = fmaxf(M, sm[w]);
+  if (warp != 0) return;
+  const int warps = blockDim.x >> 5;
+  for (int w = 1; w < warps; ++w) M = fmaxf(M, sm[w]);
   const float ref = M == -INFINITY ? 0.f : M;
-  for (int dim = threadIdx.x; dim < D; dim += blockDim.x) {
-    float sum = 0.f;
-    L = 0.f;
-    for (int w = 0; w < kW; ++w) {
-      const float f = ex2(sm[w] - ref);
-      L += sl[w] * f;
-      sum += so[w][dim] * f;
-    }
-    A.out[b * A.os[0] + h * A.os[1] + (int64_t)t * A.os[2] + dim] =
-        __float2bfloat16_rn(L == 0.f ? 0.f : sum / L);
-    if (dim == 0) A.lse[((int64_t)b * A.C.H + h) * A.S.n + t] = att_lse(M, L);
+  float sum = 0.f;
+  L = 0.f;
+  for (int w = 0; w < warps; ++w) {
+    const float f = ex2(sm[w] - ref);
+    L += sl[w] * f;
+    sum += so[w][lane] * f;
   }
+  const int grp = seg % A.groups, bh = seg / A.groups, t = grp * kAttRows + row;
+  const int b = bh / A.C.H, h = bh - b * A.C.H;
+  A.out[b * A.os[0] + h * A.os[1] + (int64_t)t * A.os[2] + dim0 + lane] =
+      __float2bfloat16_rn(L == 0.f ? 0.f : sum / L);
+  if (lane == 0 && dim0 == 0) A.lse[((int64_t)b * A.C.H + h) * A.S.n + t] = att_lse(M, L);
 }
 
 }  // namespace lsh

@@ -182,7 +182,7 @@ AttendLayout attend_layout(const lsh_cache_desc& c, const lsh_cache_rows& r) {
   const int warps = c.d == 64 ? AttCfg<64, false>::kWarps : AttCfg<128, false>::kWarps;
   const size_t rows = (size_t)L.blocks * warps * 2 * kAttRows;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-  L.ml = up((size_t)L.segments * sizeof(int2));
+  L.ml = up((size_t)L.segments * sizeof(int4));
   L.part = L.ml + up(rows * 2 * sizeof(float));
   L.total = L.part + up(rows * c.d * sizeof(float));
   return L;
@@ -205,10 +205,10 @@ lsh_status launch_attend(const AttendArgs& A, const AttendLayout& L, cudaStream_
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)L.segments, (unsigned)std::min(A.S.n, kAttRows));
+  cfg.gridDim = dim3((unsigned)L.segments, (unsigned)std::min(A.S.n, kAttRows), D / 32);
   // a segment has about this many parts where it is shared at all
   const int64_t parts = (int64_t)L.blocks * Cfg::kWarps / L.segments + 2;
-  cfg.blockDim = dim3(32u * (unsigned)std::min<int64_t>(16, std::max<int64_t>(1, parts / 8)));
+  cfg.blockDim = dim3(32u * (unsigned)std::min<int64_t>(8, (parts + 3) / 4));
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -365,7 +365,7 @@ lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
   }
   unsigned char* w = static_cast<unsigned char*>(ws);
   A.groups = L.groups;
-  A.rec = reinterpret_cast<int2*>(w);
+  A.rec = reinterpret_cast<int4*>(w);
   A.part_ml = reinterpret_cast<float*>(w + L.ml);
   A.part = reinterpret_cast<float*>(w + L.part);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
