@@ -2,6 +2,8 @@
 // it and read them back.
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "lsh_attn.h"
 #include "rope.cuh"
@@ -63,11 +65,28 @@ __device__ __forceinline__ float scale_for(float amax) {
   return ldexpf(1.f, max(e, -126));
 }
 
-// x / s rounded to the nearest integer (ties to even) in [-127, 127]; NaN to 0.
-// rs = 1 / s, a power of two, so the product is exact.
-__device__ __forceinline__ int quant(float x, float rs) {
-  const float q = fminf(fmaxf(rintf(x * rs), -127.f), 127.f);
-  return x == x ? (int)q : 0;
+// x / s rounded to the nearest integer (ties to even) in [-127, 127], NaN to 0, in
+// the low byte. rs = 1 / s is a power of two, so the product is exact; adding
+// 1.5 2^23 rounds it and leaves it in the mantissa (a conversion instruction has a
+// quarter of the rate).
+__device__ __forceinline__ uint32_t quant(float x, float rs) {
+  const float v = x == x ? fminf(fmaxf(x * rs, -127.f), 127.f) : 0.f;
+  return __float_as_uint(v + 12582912.f);
+}
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float rs) {
+  return __byte_perm(__byte_perm(quant(a, rs), quant(b, rs), 0x0040),
+                     __byte_perm(quant(c, rs), quant(d, rs), 0x0040), 0x5410);
+}
+
+// Four int8 times s, a power of two, as bf16 (exact): each byte is put into the
+// mantissa of 2^23, as q + 128, and 2^23 + 128 taken off.
+__device__ __forceinline__ uint2 i8_values(uint32_t w, float s) {
+  w ^= 0x80808080u;
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + i)) - 8388736.f) * s;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 // Four 8x8 tiles of 16-bit values, transposed: lane (g = lane / 4, t = lane % 4)
@@ -344,12 +363,9 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
         const float rs = 1.f / scales[r / C.P][1];
         float f[8];
         Vec16<bf16>::unpack(kept[k], f);
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)(quant(f[e], rs) & 255) << (8 * (e & 3));
         const int slot = (int)(base + r) & (C.P - 1);
         *reinterpret_cast<uint2*>(static_cast<int8_t*>(C.k) + page_base(C, id, h) + slot * D + dim0) =
-            make_uint2(w[0], w[1]);
+            make_uint2(quant4(f[0], f[1], f[2], f[3], rs), quant4(f[4], f[5], f[6], f[7], rs));
       }
     }
 
@@ -393,16 +409,18 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
         if (tk >= r1 || (tk + 4 <= r0 && !redo)) continue;
 #pragma unroll
         for (int k = 0; k < 2; ++k, dst += 8 * kGroup) {
-          char4 q = make_char4(0, 0, 0, 0);
-          if (!all) q = *reinterpret_cast<char4*>(dst);
+          const uint32_t fresh = quant4(bf_lo(m[2 * k]), bf_hi(m[2 * k]), bf_lo(m[2 * k + 1]),
+                                        bf_hi(m[2 * k + 1]), rs);
+          if (all) {
+            *reinterpret_cast<uint32_t*>(dst) = fresh;
+            continue;
+          }
+          char4 q = *reinterpret_cast<char4*>(dst);
           signed char* e = reinterpret_cast<signed char*>(&q);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t mw = m[2 * k + (j >> 1)];
-            if (tk + j >= r0 && tk + j < r1)
-              e[j] = (signed char)quant(j & 1 ? bf_hi(mw) : bf_lo(mw), rs);
-            else if (tk + j < r0 && redo)
-              e[j] = (signed char)rintf(e[j] * vf);
+            if (tk + j >= r0 && tk + j < r1) e[j] = (signed char)(fresh >> (8 * j));
+            else if (tk + j < r0 && redo) e[j] = (signed char)rintf(e[j] * vf);
           }
           *reinterpret_cast<char4*>(dst) = q;
         }
@@ -456,46 +474,51 @@ __global__ void __launch_bounds__(256) k_cache_gather(GatherArgs A) {
     }
     return;
   }
-  const int64_t from = page_base(C, id, h) + at % C.P * D;
+  const int64_t from = page_base(C, id, h) + (at & (C.P - 1)) * D;
   const int64_t hs = (int64_t)id * C.H + h;
   bf16* tl = tile[warp];
+  // every load of the group before the first is used: 16 bytes of v, and of x
+  // what makes 16 bytes of a row
+  constexpr int kV = I8 ? D / 32 : D / 16, kK = D / 16;
+  using Raw = std::conditional_t<I8, uint2, uint4>;
+  uint4 vr[kV];
+  Raw kr[kK];
+  const unsigned char* vg = static_cast<const unsigned char*>(C.v) + from * (I8 ? 1 : 2);
+  const unsigned char* kg = static_cast<const unsigned char*>(C.k) + from * (I8 ? 1 : 2);
+#pragma unroll
+  for (int k = 0; k < kV; ++k) vr[k] = *reinterpret_cast<const uint4*>(vg + (k * 32 + lane) * 16);
+#pragma unroll
+  for (int k = 0; k < kK; ++k) kr[k] = *reinterpret_cast<const Raw*>(kg + (k * 32 + lane) * sizeof(Raw));
+  float ks = 1.f, vs = 1.f;
   if constexpr (I8) {
-    const float vs = C.vscale[hs];
-#pragma unroll
-    for (int dim = lane; dim < D; dim += 32) {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<int8_t*>(C.v) + from + dim * kGroup);
-      const signed char* e = reinterpret_cast<const signed char*>(&u);
-      alignas(16) bf16 o[kGroup];
-#pragma unroll
-      for (int k = 0; k < kGroup; ++k) o[k] = __float2bfloat16_rn(e[k] * vs);
-      *reinterpret_cast<uint4*>(tl + dim * kRow) = *reinterpret_cast<uint4*>(o);
-      *reinterpret_cast<uint4*>(tl + dim * kRow + 8) = *reinterpret_cast<uint4*>(o + 8);
-    }
-  } else {
-#pragma unroll
-    for (int k = lane; k < 2 * D; k += 32)
-      *reinterpret_cast<uint4*>(tl + (k >> 1) * kRow + (k & 1) * 8) =
-          *reinterpret_cast<const uint4*>(static_cast<bf16*>(C.v) + from + k * 8);
+    ks = C.kscale[hs];
+    vs = C.vscale[hs];
   }
-  const float ks = I8 ? C.kscale[hs] : 1.f;
 #pragma unroll
-  for (int k = lane; k < kGroup * (D / 8); k += 32) {
-    const int r = k / (D / 8), piece = k % (D / 8);
+  for (int k = 0; k < kV; ++k) {
+    if constexpr (I8) {  // dimension 32 k + lane, 16 tokens
+      const uint2 a = i8_values(vr[k].x, vs), b = i8_values(vr[k].y, vs);
+      const uint2 c = i8_values(vr[k].z, vs), d = i8_values(vr[k].w, vs);
+      *reinterpret_cast<uint4*>(tl + (k * 32 + lane) * kRow) = make_uint4(a.x, a.y, b.x, b.y);
+      *reinterpret_cast<uint4*>(tl + (k * 32 + lane) * kRow + 8) = make_uint4(c.x, c.y, d.x, d.y);
+    } else {
+      const int p = k * 32 + lane;
+      *reinterpret_cast<uint4*>(tl + (p >> 1) * kRow + (p & 1) * 8) = vr[k];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kK; ++k) {
+    const int p = k * 32 + lane, r = p / (D / 8), piece = p % (D / 8);
     const int64_t i = i0 + r;
     if (i < 0 || i >= A.S.n) continue;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (i < nv) {
-      if constexpr (I8) {
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<int8_t*>(C.k) + from + k * 8);
-        const signed char* e = reinterpret_cast<const signed char*>(&w);
-        alignas(16) bf16 o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __float2bfloat16_rn(e[j] * ks);
-        u = *reinterpret_cast<uint4*>(o);
-      } else {
-        u = *reinterpret_cast<const uint4*>(static_cast<bf16*>(C.k) + from + k * 8);
-      }
+    uint4 u;
+    if constexpr (I8) {
+      const uint2 a = i8_values(kr[k].x, ks), b = i8_values(kr[k].y, ks);
+      u = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      u = kr[k];
     }
+    if (i >= nv) u = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(xo + i * A.xs[2] + piece * 8) = u;
   }
   __syncwarp();

@@ -270,6 +270,9 @@ def test_append_extremes():
             lb.lsh_cache_append(gpu, row.cuda(), row.cuda(), table.cuda(),
                                 torch.zeros(1, dtype=torch.int32, device=DEV))
             same_cache(gpu, ref)
+            for got, want in zip(lb.lsh_cache_gather(gpu, table.cuda(), torch.zeros(1, dtype=torch.int32, device=DEV), 1),
+                                 oc.read(ref, table, 0, 0, 1)):
+                assert torch.equal(got[0, 0].double().cpu(), want)
             assert gpu.get_device_status() == 0
     ref = oc.empty(2, H, page, d, True)
     gpu = to_gpu(ref)
