@@ -65,6 +65,11 @@ __device__ __forceinline__ float scale_for(float amax) {
   return ldexpf(1.f, max(e, -126));
 }
 
+// 1 / s of a power of two s in [2^-126, 2^126].
+__device__ __forceinline__ float recip2(float s) {
+  return __uint_as_float(0x7f000000u - __float_as_uint(s));
+}
+
 // x / s rounded to the nearest integer (ties to even) in [-127, 127], NaN to 0, in
 // the low byte. rs = 1 / s is a power of two, so the product is exact; adding
 // 1.5 2^23 rounds it and leaves it in the mantissa (a conversion instruction has a
@@ -132,25 +137,31 @@ constexpr size_t append_smem(int rows, int d, int pairs, int buffers) {
 // Tiles of two heads, unless 128 rows of 128 leave room for one.
 constexpr int append_buffers(int d, int rows) { return d * rows > 128 * 64 ? 1 : 2; }
 
-// 1/||x|| of a row whose kLanes lanes hold its values by eight. The row is scaled
-// by a power of two near its largest value, so that no square is lost.
+// 1/||x|| of a row whose kLanes lanes hold its values by eight; of a row that is
+// not there (not `in`), anything.
 template <int kLanes>
-__device__ __forceinline__ float inv_norm(const float (&f)[8]) {
-  float m = 0.f, ss = 0.f;
+__device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) ss = fmaf(f[k], f[k], ss);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+  const bool plain = !in || (ss > 0x1p-80f && ss < 0x1p100f);  // no square was lost
+  if (__all_sync(~0u, plain)) return rsqrtf(ss);
+  // scaled by a power of two near the row's largest value
+  float m = 0.f;
+  ss = 0.f;
 #pragma unroll
   for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(f[k]));
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  // the exponent of m; 0 for a zero row's and an infinity's
-  const int e = (int)(__float_as_uint(m) >> 23) - 127;
-  const bool plain = e > -127 && e < 127;
-  const float up = plain ? __uint_as_float((uint32_t)(127 - e) << 23) : e > 0 ? 0x1p-126f : 0x1p126f;
-  const float down = plain ? __uint_as_float((uint32_t)(127 + e) << 23) : e > 0 ? 0x1p126f : 0x1p-126f;
+  const int e = max(-126, min(126, (int)(__float_as_uint(m) >> 23) - 127));
+  const float up = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
   for (int k = 0; k < 8; ++k) ss = fmaf(f[k] * up, f[k] * up, ss);
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-  const float norm = sqrtf(ss) * down;
+  const float norm = sqrtf(ss) * __uint_as_float((uint32_t)(127 + e) << 23);
   return norm < 0x1p-126f ? 0.f : 1.f / norm;
 }
 
@@ -210,18 +221,23 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   int* amax = reinterpret_cast<int*>(st + R * pstride);
   __shared__ int ids[8];  // pages of the block's tokens
   __shared__ float scales[2][4];  // of a page: x old, new, v old, new
+  __shared__ uint2 phase[D / 2];
+  __shared__ uint8_t axis[D / 2];
 
+  // a thread's pieces are the same dimensions of rows 256 / kPieces apart
+  constexpr int kStep = 256 / kPieces;
+  const int dim0 = tid % kPieces * 8, row0 = tid / kPieces;
   auto fetch = [&](int h) {
-    bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride;
-    bf16* vt = xt + R * kStride;
-    const int own = (r1 - r0) * kPieces;
-    const bf16* xg = A.x + b * A.xs[0] + h * A.xs[1];
-    const bf16* vg = A.v + b * A.vs[0] + h * A.vs[1];
-    for (int i = tid; i < own; i += 256) {
-      const int r = r0 + i / kPieces, piece = i % kPieces;
-      const int64_t t = tok0 + r;
-      sm100::cp_async16_zfill(xt + r * kStride + piece * 8, xg + t * A.xs[2] + piece * 8, true);
-      sm100::cp_async16_zfill(vt + r * kStride + piece * 8, vg + t * A.vs[2] + piece * 8, true);
+    bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride + row0 * kStride + dim0;
+    const bf16* xg = A.x + b * A.xs[0] + h * A.xs[1] + (int64_t)(tok0 + row0) * A.xs[2] + dim0;
+    const bf16* vg = A.v + b * A.vs[0] + h * A.vs[1] + (int64_t)(tok0 + row0) * A.vs[2] + dim0;
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) {
+      const int r = row0 + k * kStep;
+      if (r >= r0 && r < r1) {
+        sm100::cp_async16_zfill(xt + k * kStep * kStride, xg + k * kStep * A.xs[2], true);
+        sm100::cp_async16_zfill(xt + (R + k * kStep) * kStride, vg + k * kStep * A.vs[2], true);
+      }
     }
     sm100::cp_async_commit();
   };
@@ -236,19 +252,23 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     }
     ids[tid] = id;
   }
+  P8 piece;
   if constexpr (TURN != kTurnNone) {
     const int pairs = A.rot.pairs;
-    for (int i = tid; i < (r1 - r0) * pairs; i += 256) {
-      const int r = r0 + i / pairs, p = i % pairs;
-      const int ax = rot_axis(A.rot, p);
-      rot_angle(A.pos[ax * A.pos_axis + b * A.pos_batch + tok0 + r], A.freqs[p],
-                &ct[r * pstride + p], &st[r * pstride + p]);
+    if (tid < pairs) {
+      phase[tid] = rot_phase(A.freqs[tid]);
+      axis[tid] = (uint8_t)rot_axis(A.rot, tid);
     }
+    __syncthreads();
+    const int32_t* pos = A.pos + b * A.pos_batch + tok0;
+    // rows go round a warp at a time: lanes take neighbouring pairs
+    for (int r = r0 + warp; r < r1; r += 8)
+      for (int p = lane; p < pairs; p += 32)
+        rot_angle<true>(pos[axis[p] * A.pos_axis + r], phase[p], &ct[r * pstride + p],
+                        &st[r * pstride + p]);
+    piece.place(A.rot, dim0);
   }
-  // a thread's pieces are the same dimensions of rows 256 / kPieces apart
-  const int dim0 = tid % kPieces * 8, row0 = tid / kPieces;
-  P8 piece;
-  if constexpr (TURN != kTurnNone) piece.place(A.rot, dim0);
+  const int pmask = C.P - 1, pshift = __ffs(C.P) - 1, off0 = (int)base & pmask;  // off0: row 0's slot
 
   for (int h = h0; h < h1; ++h) {
     if (kBuf == 2 && h + 1 < h1) {
@@ -261,21 +281,22 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     __syncthreads();
     const bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride;
     const bf16* vt = xt + R * kStride;
-    bf16* xo = A.xr ? A.xr + b * A.os[0] + h * A.os[1] + dim0 : nullptr;
+    bf16* xo = A.xr ? A.xr + b * A.os[0] + h * A.os[1] + (int64_t)(tok0 + row0) * A.os[2] + dim0 : nullptr;
 
     uint4 kept[I8 ? kPass : 1];
 #pragma unroll
     for (int k = 0; k < kPass; ++k) {
-      const int r = row0 + k * (256 / kPieces);
+      const int r = row0 + k * kStep;
       const bool in = r >= r0 && r < r1;
       const bf16* row = xt + r * kStride;
       float f[8];
       uint4 u = *reinterpret_cast<const uint4*>(row + dim0);
       Vec16<bf16>::unpack(u, f);
-      const float inv = inv_norm<kPieces>(f);
-      const int id = ids[r / C.P];
-      const int slot = (int)(base + r) & (C.P - 1);
-      if (in && id >= 0 && dim0 == 0) C.kinv[((int64_t)id * C.H + h) * C.P + slot] = inv;
+      const float inv = inv_norm<kPieces>(f, in);
+      const int pg = r >> pshift, id = ids[pg];
+      // the row's slot in its page (page_base of id: [P][D] a head)
+      const int64_t at = ((int64_t)id * C.H + h) * C.P + ((off0 + r) & pmask);
+      if (in && id >= 0 && dim0 == 0) C.kinv[at] = inv;
       if constexpr (TURN != kTurnNone) {
         float y[8], c[P8::kPairs], s[P8::kPairs];
         if constexpr (ADJ) {
@@ -294,32 +315,41 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
         piece.turn(f, y, c, s);
         u = pack16<bf16>(f);
       }
-      if (in && xo) *reinterpret_cast<uint4*>(xo + (int64_t)(tok0 + r) * A.os[2]) = u;
+      if (in && xo) *reinterpret_cast<uint4*>(xo + k * kStep * A.os[2]) = u;
       if constexpr (I8) {
         kept[k] = u;
-        float g[8];
-        Vec16<bf16>::unpack(u, f);
-        load_w<bf16, 8>(vt + r * kStride + dim0, g);
-        float km = 0.f, vm = 0.f;
-        bool odd = false;
+        // largest magnitudes, as bits with the sign taken off: finite ones compare
+        // like integers; infinities and NaN are above 0x7f7f and left out
+        uint32_t km = 0, vm = 0;
+        const uint4 w = *reinterpret_cast<const uint4*>(vt + r * kStride + dim0);
+        const uint32_t ku[4] = {u.x, u.y, u.z, u.w}, vu[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const bool fk = fabsf(f[e]) <= 3.4e38f, gk = fabsf(g[e]) <= 3.4e38f;
-          km = fk ? fmaxf(km, fabsf(f[e])) : km;
-          vm = gk ? fmaxf(vm, fabsf(g[e])) : vm;
-          odd |= !fk || !gk;
+        for (int e = 0; e < 4; ++e) {
+          km = __vmaxu2(km, ku[e] & 0x7fff7fffu);
+          vm = __vmaxu2(vm, vu[e] & 0x7fff7fffu);
         }
-        if (!in) km = vm = 0.f;
-        if (in && odd) cache_error(C);
+        km = max(km & 0xffffu, km >> 16);
+        vm = max(vm & 0xffffu, vm >> 16);
+        if (in && max(km, vm) > 0x7f7fu) {
+          cache_error(C);
+          km = vm = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t a = ku[e >> 1] >> (16 * (e & 1)) & 0x7fffu, c = vu[e >> 1] >> (16 * (e & 1)) & 0x7fffu;
+            if (a <= 0x7f7fu) km = max(km, a);
+            if (c <= 0x7f7fu) vm = max(vm, c);
+          }
+        }
+        if (!in) km = vm = 0;
         // a warp's rows of a pass lie in one page of 16 at least
-        km = warp_max(km);
-        vm = warp_max(vm);
+        km = __reduce_max_sync(~0u, km);
+        vm = __reduce_max_sync(~0u, vm);
         if (lane == 0) {
-          atomicMax(&amax[2 * (r / C.P)], __float_as_int(km));
-          atomicMax(&amax[2 * (r / C.P) + 1], __float_as_int(vm));
+          atomicMax(&amax[2 * pg], (int)(km << 16));
+          atomicMax(&amax[2 * pg + 1], (int)(vm << 16));
         }
       } else if (in && id >= 0) {
-        *reinterpret_cast<uint4*>(static_cast<bf16*>(C.k) + page_base(C, id, h) + slot * D + dim0) = u;
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(C.k) + at * D + dim0) = u;
       }
     }
 
@@ -358,13 +388,13 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       }
 #pragma unroll
       for (int k = 0; k < kPass; ++k) {
-        const int r = row0 + k * (256 / kPieces), id = ids[r / C.P];
+        const int r = row0 + k * kStep, id = ids[r >> pshift];
         if (r < r0 || r >= r1 || id < 0) continue;
-        const float rs = 1.f / scales[r / C.P][1];
+        const float rs = recip2(scales[r >> pshift][1]);
         float f[8];
         Vec16<bf16>::unpack(kept[k], f);
-        const int slot = (int)(base + r) & (C.P - 1);
-        *reinterpret_cast<uint2*>(static_cast<int8_t*>(C.k) + page_base(C, id, h) + slot * D + dim0) =
+        const int64_t at = ((int64_t)id * C.H + h) * C.P + ((off0 + r) & pmask);
+        *reinterpret_cast<uint2*>(static_cast<int8_t*>(C.k) + at * D + dim0) =
             make_uint2(quant4(f[0], f[1], f[2], f[3], rs), quant4(f[4], f[5], f[6], f[7], rs));
       }
     }
@@ -381,9 +411,9 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       const int trow = rb + (i >> 1) * 4 + (i & 1) + 2 * (tile & 1);
       uint32_t m[4];
       ldsm_x4_trans(m, vt + trow * kStride + d0 + 8 * (tile >> 1));
-      const int id = ids[rb / C.P];
+      const int id = ids[rb >> pshift];
       if (id < 0) continue;
-      const int64_t at = page_base(C, id, h) + ((base + rb) & (C.P - 1)) * D +
+      const int64_t at = (((int64_t)id * C.H + h) * C.P + ((off0 + rb) & pmask)) * D +
                          (d0 + (lane >> 2)) * kGroup + (lane & 3) * 4;
       const int tk = rb + (lane & 3) * 4;
       const bool all = tk >= r0 && tk + 4 <= r1;
@@ -403,9 +433,9 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
         }
       } else {
         int8_t* dst = static_cast<int8_t*>(C.v) + at;
-        const float rs = 1.f / scales[rb / C.P][3];
+        const float rs = recip2(scales[rb >> pshift][3]);
         const bool redo = again && tk < r0;
-        const float vf = redo ? scales[rb / C.P][2] * rs : 1.f;
+        const float vf = redo ? scales[rb >> pshift][2] * rs : 1.f;
         if (tk >= r1 || (tk + 4 <= r0 && !redo)) continue;
 #pragma unroll
         for (int k = 0; k < 2; ++k, dst += 8 * kGroup) {

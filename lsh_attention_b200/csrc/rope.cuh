@@ -2,9 +2,11 @@
 //
 // Pair (lo, hi) turns by t = position of its axis * frequency:
 //   lo' = lo cos t - hi sin t,   hi' = lo sin t + hi cos t.
-// t reaches millions of turns, so it is formed and reduced to a fraction of a
-// turn in fp64 (the product of an int32 and an fp32 is exact there up to 2^29);
-// the sine and cosine of the fraction are fp32.
+// t reaches millions of turns, of which only the fraction of a turn counts. A
+// frequency is therefore held as a fraction of a turn in 64 bits of fixed point:
+// a position times it, modulo 2^64, is the fraction, exact but for the position
+// times 2^-65, in three integer operations (products in fp64, reduced there, took
+// a third of the instructions of a kernel that has to keep up with DRAM).
 #pragma once
 
 #include "common.cuh"
@@ -29,11 +31,29 @@ __device__ __forceinline__ int rot_axis(const RotPlan& r, int p) {
   return a;
 }
 
-// cos and sin of position * frequency.
-__device__ __forceinline__ void rot_angle(int32_t pos, float freq, float* c, float* s) {
-  double turns = (double)pos * (double)freq * 0.15915494309189533577;  // 1 / (2 pi)
-  turns -= rint(turns);
-  sincospif(2.0f * (float)turns, s, c);
+// A frequency, radians a position, as a fraction of a turn in units of 2^-64.
+// 1 / (2 pi) is taken to 107 bits, so that the product is good to 2^-64.
+__device__ __forceinline__ uint2 rot_phase(float freq) {
+  const double f = (double)freq, hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  const double p = f * hi, e = fma(f, hi, -p) + f * lo;
+  // the fraction of p in [0, 1) has 53 bits; what is left of p is below 2^-53 of it
+  const uint64_t u = (uint64_t)((p - floor(p)) * 0x1p64) + (uint64_t)(int64_t)(e * 0x1p64);
+  return make_uint2((uint32_t)u, (uint32_t)(u >> 32));
+}
+
+// cos and sin of position * frequency. FAST: the sine and cosine units, off by
+// 2^-21 at most: for results that are rounded to bf16.
+template <bool FAST>
+__device__ __forceinline__ void rot_angle(int32_t pos, uint2 phase, float* c, float* s) {
+  // bits 32 .. 63 of pos * phase, pos being signed
+  const uint32_t p = (uint32_t)pos;
+  const int32_t turn =
+      (int32_t)(__umulhi(p, phase.x) + p * phase.y - (pos < 0 ? phase.x : 0u));
+  if constexpr (FAST) {
+    __sincosf((float)turn * 1.46291807926715968e-9f, s, c);  // 2 pi / 2^32: [-pi, pi]
+  } else {
+    sincospif((float)turn * 0x1p-31f, s, c);
+  }
 }
 
 // W consecutive elements of T (W = 1 too), loaded as one access, as fp32.
@@ -151,13 +171,21 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
   constexpr int N = 16 / sizeof(T), kPieces = D / N;  // a row's pieces lie in one warp
   constexpr int kTok = 256 / kPieces;
   using P = Piece<N, W, ADJ>;
+  constexpr bool kFast = sizeof(T) == 2;
   __shared__ float ct[ADJ ? 1 : kTok * D / 2], st[ADJ ? 1 : kTok * D / 2];
+  __shared__ uint2 phase[D / 2];
+  __shared__ uint8_t axis[D / 2];
   __shared__ uint4 swap[ADJ ? 1 : kRopeHeads][256];
   const int64_t tok0 = (int64_t)blockIdx.x * kTok;
   const int tl = threadIdx.x / kPieces, dim0 = threadIdx.x % kPieces * N;
   const int64_t tok = tok0 + tl;
   const bool in = tok < A.n;
   const int pairs = A.rot.pairs;
+  if (threadIdx.x < pairs) {
+    phase[threadIdx.x] = rot_phase(A.freqs[threadIdx.x]);
+    axis[threadIdx.x] = (uint8_t)rot_axis(A.rot, threadIdx.x);
+  }
+  __syncthreads();
   P piece;
   piece.place(A.rot, dim0);
   for (int64_t bg = blockIdx.y; bg < (int64_t)A.B * A.head_groups; bg += gridDim.y) {
@@ -172,7 +200,7 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
       const int toks = (int)min((int64_t)kTok, A.n - tok0);
       for (int i = threadIdx.x; i < toks * pairs; i += 256) {
         const int p = i % pairs;
-        rot_angle(pos[rot_axis(A.rot, p) * A.pos_axis + tok0 + i / pairs], A.freqs[p], &ct[i], &st[i]);
+        rot_angle<kFast>(pos[axis[p] * A.pos_axis + tok0 + i / pairs], phase[p], &ct[i], &st[i]);
       }
       __syncthreads();
     }
@@ -183,7 +211,7 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
       if (in && (piece.turned >> i & 1)) {
         const int p = piece.pair_of(i);
         if constexpr (ADJ) {
-          rot_angle(pos[rot_axis(A.rot, p) * A.pos_axis + tok], A.freqs[p], &c[i], &s[i]);
+          rot_angle<kFast>(pos[axis[p] * A.pos_axis + tok], phase[p], &c[i], &s[i]);
         } else {
           c[i] = ct[tl * pairs + p];
           s[i] = st[tl * pairs + p];

@@ -2,9 +2,10 @@
 oracle/cache.py (float64).
 
 Tolerances. A rounding to bf16 is off by at most 2^-8 of the value, one to fp32 by 2^-24.
-* Rotation: the fraction of a turn is held in fp32 (below 1/2: off by 2^-26 turns, 2 pi 2^-26 =
-  2^-23.3 rad), its sine and cosine are good to two steps (2^-23); two products and a sum add
-  3 * 2^-24 of |lo| + |hi|. Together below 2^-21 (|lo| + |hi|), then the result's own rounding.
+* Rotation: the fraction of a turn is rounded to fp32 (below 1/2: off by 2^-26 turns, 2 pi 2^-26 =
+  2^-23.3 rad), its sine and cosine are good to two steps (2^-23) for fp32 rows and to 2^-21.1, the
+  sine unit's bound, for bf16 ones; two products and a sum add 3 * 2^-24 of |lo| + |hi|. Together
+  below 2^-21 (fp32) and 2^-20 (bf16) of |lo| + |hi|, then the result's own rounding.
 * 1/||x||: a sum of d <= 128 squares in runs of 8 and a tree (at most 16 roundings), a root, a
   product and a quotient: below 20 * 2^-24 of it.
 * Attention: a logit's sum of d products is off by d 2^-24 ||x|| (Cauchy-Schwarz with unit keys),
@@ -53,7 +54,7 @@ def near(got, ref, tol, what):
 
 
 def rope_tol(x, dims, adjacent, eps):
-    """2^-21 (|lo| + |hi|) and the rounding of the result, per element."""
+    """2^-21 or 2^-20 (|lo| + |hi|) and the rounding of the result, per element."""
     size = x.double().abs()
     at = 0
     pair = size.clone()
@@ -64,7 +65,7 @@ def rope_tol(x, dims, adjacent, eps):
         pair[..., at:at + d] = sec + other
         at += d
     # the result is at most |lo| + |hi|
-    return pair * (2.0 ** -21 + eps)
+    return pair * ((2.0 ** -21 if x.dtype == torch.float32 else 2.0 ** -20) + eps)
 
 
 # ------------------------------------------------------------------------------ rotary positions
