@@ -478,18 +478,6 @@ def _check_angles(positions, freqs, axis_dims: tuple, B: int, n: int) -> bool:
     return batched
 
 
-@functools.lru_cache(maxsize=1024)
-def _rope_desc(B, H, n, d, dtype, inverse, batched, axis_dims, adjacent, xs, os_) -> LshRopeDesc:
-    return LshRopeDesc(B, H, n, d, dtype, inverse, batched, _axes(axis_dims, adjacent),
-                       (ctypes.c_int64 * 3)(*xs), (ctypes.c_int64 * 3)(*os_))
-
-
-@functools.lru_cache(maxsize=1024)
-def _cache_rows(B, n, max_pages, batched, xs, vs=(0, 0, 0), os_=(0, 0, 0)) -> LshCacheRows:
-    three = ctypes.c_int64 * 3
-    return LshCacheRows(B, n, max_pages, batched, three(*xs), three(*vs), three(*os_))
-
-
 def _raw_stream(device) -> int:
     """Handle of the device's current stream: what _stream(None) gives, without making a Stream
     object (which takes longer than a small kernel)."""
@@ -506,6 +494,24 @@ def _on_stream(stream, call, *tensors):
         return call()
 
 
+#: what a call's checks found, by what they looked at: shapes, strides, types and devices of its
+#: tensors (nothing of their memory). A step of a loop is checked once.
+_plans: dict = {}
+
+
+def _seen(*tensors) -> tuple:
+    """What the checks look at of every tensor."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+                  for t in tensors])
+
+
+def _keep(key, plan):
+    if len(_plans) >= 4096:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
 def lsh_rope(x, positions, freqs, *, axis_dims, adjacent: bool = False, inverse: bool = False,
              out=None, stream=None):
     """Rotary positions on the rows of x [B, H, n, d] (fp32 or bf16; any strides with the last
@@ -514,24 +520,33 @@ def lsh_rope(x, positions, freqs, *, axis_dims, adjacent: bool = False, inverse:
     for each pair). `adjacent`: pairs are neighbouring dimensions, else the halves of an axis.
     `inverse` turns back, which is the gradient with respect to x. Returns out [B, H, n, d];
     out may be x itself."""
-    _on_current_device(stream, x=x, positions=positions, freqs=freqs, out=out)
     if stream is not None:
+        _on_current_device(stream, x=x, positions=positions, freqs=freqs, out=out)
         return _on_stream(stream, lambda: lsh_rope(x, positions, freqs, axis_dims=axis_dims,
                                                    adjacent=adjacent, inverse=inverse, out=out),
                           x, positions, freqs, out)
-    B, H, n, d = x.shape
+    key = ("rope", torch.cuda.current_device(), tuple(axis_dims), adjacent, inverse,
+           _seen(x, positions, freqs, out))
+    desc = _plans.get(key) or _keep(key, _plan_rope(x, positions, freqs, key[2], adjacent, inverse,
+                                                    out))
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check((_lib or load()).lsh_rope(desc, x.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
+                                     out.data_ptr(), _raw_stream(x.device)))
+    return out
+
+
+def _plan_rope(x, positions, freqs, axis_dims, adjacent, inverse, out):
+    _on_current_device(None, x=x, positions=positions, freqs=freqs, out=out)
+    B, H, n, d = shape = tuple(x.shape)
     if x.dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {x.dtype}")
-    axis_dims = tuple(axis_dims)
-    xs = _rows_strides(x, "x", x.dtype, (B, H, n, d))
+    xs = _rows_strides(x, "x", x.dtype, shape)
     batched = _check_angles(positions, freqs, axis_dims, B, n)
-    if out is None:
-        out = torch.empty((B, H, n, d), dtype=x.dtype, device=x.device)
-    desc = _rope_desc(B, H, n, d, _DTYPES[x.dtype], int(inverse), batched, axis_dims, adjacent,
-                      xs, _rows_strides(out, "out", x.dtype, (B, H, n, d)))
-    _check(load().lsh_rope(ctypes.byref(desc), x.data_ptr(), positions.data_ptr(),
-                           freqs.data_ptr(), out.data_ptr(), _raw_stream(x.device)))
-    return out
+    three = ctypes.c_int64 * 3
+    os_ = (H * n * d, n * d, d) if out is None else _rows_strides(out, "out", x.dtype, shape)
+    return ctypes.byref(LshRopeDesc(B, H, n, d, _DTYPES[x.dtype], int(inverse), batched,
+                                    _axes(axis_dims, adjacent), three(*xs), three(*os_)))
 
 
 class LshCache:
@@ -570,6 +585,8 @@ class LshCache:
                                  LSH_CACHE_I8 if self.int8 else LSH_CACHE_BF16)
         self.memory = LshCacheMemory(*[None if t is None else t.data_ptr()
                                        for t in self.tensors.values()])
+        self.desc_ref, self.memory_ref = ctypes.byref(self.desc), ctypes.byref(self.memory)
+        self.kind = (pages, heads, page, d, self.int8, k.device)
 
     @classmethod
     def empty(cls, pages: int, heads: int, page_size: int, d: int, *, int8: bool = False,
@@ -591,7 +608,7 @@ class LshCache:
         self.status.zero_()
 
 
-def _check_tables(cache, B: int, page_table, seq_len, n_valid, what: str = "seq_len") -> None:
+def _check_tables(B: int, page_table, seq_len, n_valid, what: str = "seq_len") -> None:
     _require(page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
     _require(seq_len, what, torch.int32, (B,))
     if n_valid is not None:
@@ -602,6 +619,17 @@ def _opt(t):
     return None if t is None else t.data_ptr()
 
 
+def _cache_rows(B, n, max_pages, batched=False, xs=(0, 0, 0), vs=(0, 0, 0), os_=(0, 0, 0)):
+    three = ctypes.c_int64 * 3
+    return LshCacheRows(B, n, max_pages, batched, three(*xs), three(*vs), three(*os_))
+
+
+def _new_rows(shape, t, name: str) -> tuple:
+    """Strides of rows that the call returns: those of `t`, or of a new tensor."""
+    B, H, n, d = shape
+    return (H * n * d, n * d, d) if t is None else _rows_strides(t, name, torch.bfloat16, shape)
+
+
 def lsh_cache_append(cache: LshCache, x, v, page_table, seq_len, *, n_valid=None, positions=None,
                      freqs=None, axis_dims=(), adjacent: bool = False, xr=None, stream=None):
     """Append the rows x, v [B, H, n, d] (bf16, any strides with the last dimension contiguous)
@@ -609,61 +637,80 @@ def lsh_cache_append(cache: LshCache, x, v, page_table, seq_len, *, n_valid=None
     lsh_rope). page_table int32 [B, max_pages], seq_len int32 [B], n_valid int32 [B] or None
     (all n rows). Returns the rotated rows [B, H, n, d] (zeros past n_valid), the queries of
     lsh_cache_attend; without a rotation and without `xr`, x itself. xr may be x."""
-    _on_current_device(stream, x=x, v=v, page_table=page_table, seq_len=seq_len, n_valid=n_valid,
-                       positions=positions, freqs=freqs, xr=xr, cache=cache.k)
     if stream is not None:
+        _on_current_device(stream, x=x, v=v, page_table=page_table, seq_len=seq_len,
+                           n_valid=n_valid, positions=positions, freqs=freqs, xr=xr, cache=cache.k)
         return _on_stream(
             stream, lambda: lsh_cache_append(
                 cache, x, v, page_table, seq_len, n_valid=n_valid, positions=positions,
                 freqs=freqs, axis_dims=axis_dims, adjacent=adjacent, xr=xr),
             x, v, page_table, seq_len, n_valid, positions, freqs, xr, *cache.tensors.values())
+    key = ("append", torch.cuda.current_device(), cache.kind, tuple(axis_dims), adjacent,
+           _seen(x, v, page_table, seq_len, n_valid, positions, freqs, xr))
+    rows, rot = _plans.get(key) or _keep(key, _plan_append(
+        cache, x, v, page_table, seq_len, n_valid, positions, freqs, key[3], adjacent, xr))
+    if xr is None and axis_dims:
+        xr = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _check((_lib or load()).lsh_cache_append(
+        cache.desc_ref, cache.memory_ref, rows, rot, x.data_ptr(), v.data_ptr(), _opt(positions),
+        _opt(freqs), page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), _opt(xr),
+        _raw_stream(x.device)))
+    return x if xr is None else xr
+
+
+def _plan_append(cache, x, v, page_table, seq_len, n_valid, positions, freqs, axis_dims, adjacent,
+                 xr):
+    _on_current_device(None, x=x, v=v, page_table=page_table, seq_len=seq_len, n_valid=n_valid,
+                       positions=positions, freqs=freqs, xr=xr, cache=cache.k)
     B, H, n, d = shape = tuple(x.shape)
     if (H, d) != (cache.heads, cache.d):
         raise ValueError(f"x has {H} heads of {d}, the cache {cache.heads} of {cache.d}")
     xs = _rows_strides(x, "x", torch.bfloat16, shape)
     vs = _rows_strides(v, "v", torch.bfloat16, shape)
-    _check_tables(cache, B, page_table, seq_len, n_valid)
-    axis_dims = tuple(axis_dims)
-    batched = False
+    _check_tables(B, page_table, seq_len, n_valid)
+    batched, os_ = False, (0, 0, 0)
     if axis_dims:
         if positions is None or freqs is None:
             raise ValueError("a rotation needs positions and freqs")
         batched = _check_angles(positions, freqs, axis_dims, B, n)
-        if xr is None:
-            xr = torch.empty(shape, dtype=x.dtype, device=x.device)
-    os_ = _rows_strides(xr, "xr", torch.bfloat16, shape) if xr is not None else (0, 0, 0)
-    rows = _cache_rows(B, n, page_table.shape[1], batched, xs, vs, os_)
-    _check(load().lsh_cache_append(
-        ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows),
-        ctypes.byref(_axes(axis_dims, adjacent)), x.data_ptr(), v.data_ptr(), _opt(positions),
-        _opt(freqs), page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), _opt(xr),
-        _raw_stream(x.device)))
-    return x if xr is None else xr
+    if axis_dims or xr is not None:
+        os_ = _new_rows(shape, xr, "xr")
+    return (ctypes.byref(_cache_rows(B, n, page_table.shape[1], batched, xs, vs, os_)),
+            ctypes.byref(_axes(axis_dims, adjacent)))
 
 
 def lsh_cache_gather(cache: LshCache, page_table, start, n: int, *, n_valid=None, x=None, v=None,
                      stream=None):
     """Read n rows from position start[b] of every sequence back as values. start int32 [B],
     n_valid int32 [B] or None. Returns x, v [B, H, n, d] bf16, zeros past n_valid."""
-    _on_current_device(stream, page_table=page_table, start=start, n_valid=n_valid, x=x, v=v,
-                       cache=cache.k)
     if stream is not None:
+        _on_current_device(stream, page_table=page_table, start=start, n_valid=n_valid, x=x, v=v,
+                           cache=cache.k)
         return _on_stream(stream, lambda: lsh_cache_gather(cache, page_table, start, n,
                                                            n_valid=n_valid, x=x, v=v),
                           page_table, start, n_valid, x, v, *cache.tensors.values())
+    key = ("gather", torch.cuda.current_device(), cache.kind, n,
+           _seen(page_table, start, n_valid, x, v))
+    rows, shape = _plans.get(key) or _keep(key, _plan_gather(cache, page_table, start, n, n_valid,
+                                                             x, v))
+    if x is None:
+        x = torch.empty(shape, dtype=torch.bfloat16, device=page_table.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=page_table.device)
+    _check((_lib or load()).lsh_cache_gather(
+        cache.desc_ref, cache.memory_ref, rows, page_table.data_ptr(), start.data_ptr(),
+        _opt(n_valid), x.data_ptr(), v.data_ptr(), _raw_stream(page_table.device)))
+    return x, v
+
+
+def _plan_gather(cache, page_table, start, n, n_valid, x, v):
+    _on_current_device(None, page_table=page_table, start=start, n_valid=n_valid, x=x, v=v,
+                       cache=cache.k)
     B = page_table.shape[0]
     shape = (B, cache.heads, n, cache.d)
-    _check_tables(cache, B, page_table, start, n_valid, "start")
-    x, v = (torch.empty(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None else t
-            for t in (x, v))
-    rows = _cache_rows(B, n, page_table.shape[1], False,
-                       _rows_strides(x, "x", torch.bfloat16, shape),
-                       _rows_strides(v, "v", torch.bfloat16, shape))
-    _check(load().lsh_cache_gather(
-        ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows),
-        page_table.data_ptr(), start.data_ptr(), _opt(n_valid), x.data_ptr(), v.data_ptr(),
-        _raw_stream(x.device)))
-    return x, v
+    _check_tables(B, page_table, start, n_valid, "start")
+    return (ctypes.byref(_cache_rows(B, n, page_table.shape[1], False, _new_rows(shape, x, "x"),
+                                     _new_rows(shape, v, "v"))), shape)
 
 
 def lsh_cache_attend(cache: LshCache, x, page_table, seq_len, *, n_valid=None, out=None, lse=None,
@@ -672,50 +719,54 @@ def lsh_cache_attend(cache: LshCache, x, page_table, seq_len, *, n_valid=None, o
     lsh_cache_append has stored them: x [B, H, n, d] bf16, the rotated rows that it returned,
     with its page_table, seq_len (before those tokens) and n_valid. Returns out [B, H, n, d]
     bf16 and lse [B, H, n] fp32; rows past n_valid are zeros and -inf."""
-    _on_current_device(stream, x=x, page_table=page_table, seq_len=seq_len, n_valid=n_valid,
-                       out=out, lse=lse, ws=ws, cache=cache.k)
     if stream is not None:
+        _on_current_device(stream, x=x, page_table=page_table, seq_len=seq_len, n_valid=n_valid,
+                           out=out, lse=lse, ws=ws, cache=cache.k)
         return _on_stream(stream, lambda: lsh_cache_attend(cache, x, page_table, seq_len,
                                                            n_valid=n_valid, out=out, lse=lse,
                                                            ws=ws),
                           x, page_table, seq_len, n_valid, out, lse, ws, *cache.tensors.values())
+    key = ("attend", torch.cuda.current_device(), cache.kind,
+           _seen(x, page_table, seq_len, n_valid, out, lse, ws))
+    rows, need = _plans.get(key) or _keep(key, _plan_attend(cache, x, page_table, seq_len, n_valid,
+                                                            out, lse, ws))
+    device = x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    if lse is None:
+        lse = torch.empty(x.shape[:3], dtype=torch.float32, device=device)
+    stream = _raw_stream(device)
+    if ws is None and torch.cuda.is_current_stream_capturing():
+        # a graph keeps its own workspace: the cached one may grow and go away
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    elif ws is None:
+        ws = _ws_cache.get((device.index, stream))
+        if ws is None or ws.numel() < need:
+            ws = _scratch(device, None, need)
+    _check((_lib or load()).lsh_cache_attend(
+        cache.desc_ref, cache.memory_ref, rows, x.data_ptr(), page_table.data_ptr(),
+        seq_len.data_ptr(), _opt(n_valid), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+        ws.numel() * ws.element_size(), stream))
+    return out, lse
+
+
+def _plan_attend(cache, x, page_table, seq_len, n_valid, out, lse, ws):
+    _on_current_device(None, x=x, page_table=page_table, seq_len=seq_len, n_valid=n_valid, out=out,
+                       lse=lse, ws=ws, cache=cache.k)
     B, H, n, d = shape = tuple(x.shape)
     if (H, d) != (cache.heads, cache.d):
         raise ValueError(f"x has {H} heads of {d}, the cache {cache.heads} of {cache.d}")
     xs = _rows_strides(x, "x", torch.bfloat16, shape)
-    _check_tables(cache, B, page_table, seq_len, n_valid)
-    if out is None:
-        out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    if lse is None:
-        lse = torch.empty((B, H, n), dtype=torch.float32, device=x.device)
-    else:
+    _check_tables(B, page_table, seq_len, n_valid)
+    if lse is not None:
         _require(lse, "lse", torch.float32, (B, H, n))
-    rows = _cache_rows(B, n, page_table.shape[1], False, xs, (0, 0, 0),
-                       _rows_strides(out, "out", torch.bfloat16, shape))
-    need = _attend_workspace(B, n, H, d, cache.page_size, cache.int8)
-    stream = _raw_stream(x.device)
-    if ws is None and torch.cuda.is_current_stream_capturing():
-        # a graph keeps its own workspace: the cached one may grow and go away
-        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    elif ws is None:
-        ws = _ws_cache.get((x.device.index, stream))
-        if ws is None or ws.numel() < need:
-            ws = _scratch(x.device, None, need)
-    _check(load().lsh_cache_attend(
-        ctypes.byref(cache.desc), ctypes.byref(cache.memory), ctypes.byref(rows), x.data_ptr(),
-        page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), out.data_ptr(), lse.data_ptr(),
-        ws.data_ptr(), ws.numel() * ws.element_size(), stream))
-    return out, lse
-
-
-@functools.lru_cache(maxsize=1024)
-def _attend_workspace(B: int, n: int, heads: int, d: int, page_size: int, int8: bool) -> int:
-    desc = LshCacheDesc(1, heads, page_size, d, LSH_CACHE_I8 if int8 else LSH_CACHE_BF16)
-    out = ctypes.c_size_t(0)
-    _check(load().lsh_cache_attend_workspace_size(
-        ctypes.byref(desc), ctypes.byref(_cache_rows(B, n, 1, False, (0, 0, 0))),
-        ctypes.byref(out)))
-    return out.value
+    if ws is not None:
+        _require(ws, "ws", None, None)
+    rows = _cache_rows(B, n, page_table.shape[1], False, xs, (0, 0, 0), _new_rows(shape, out, "out"))
+    need = ctypes.c_size_t(0)
+    _check(load().lsh_cache_attend_workspace_size(cache.desc_ref, ctypes.byref(rows),
+                                                  ctypes.byref(need)))
+    return ctypes.byref(rows), need.value
 
 
 def _scratch(device, stream, need: int) -> torch.Tensor:

@@ -131,7 +131,7 @@ __host__ __device__ constexpr int append_rows(bool i8, int page) {
 // Angles of a row in shared memory, rounded up to whole float4.
 __host__ __device__ constexpr int append_pairs(int pairs) { return (pairs + 3) / 4 * 4; }
 constexpr size_t append_smem(int rows, int d, int pairs, int buffers) {
-  return (size_t)rows * (buffers * 2 * (d * 2 + 16) + append_pairs(pairs) * 8) + 128;
+  return (size_t)rows * (buffers * 2 * (d * 2 + 16) + append_pairs(pairs) * 8) + 32 + 128;
 }
 
 // Tiles of two heads, unless 128 rows of 128 leave room for one.
@@ -216,9 +216,9 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   bf16* tiles = reinterpret_cast<bf16*>(smem);  // [buffers][x, v][R][kStride]
   float* ct = reinterpret_cast<float*>(tiles + kBuf * 2 * R * kStride);
   const int pstride = append_pairs(A.rot.pairs);
-  float* st = ct + R * pstride;
+  float* st = ct + R * pstride + 4;  // behind each the angle of what is not turned
   // int8: of at most two pages, largest magnitudes of x and v
-  int* amax = reinterpret_cast<int*>(st + R * pstride);
+  int* amax = reinterpret_cast<int*>(st + R * pstride + 4);
   __shared__ int ids[8];  // pages of the block's tokens
   __shared__ float scales[2][4];  // of a page: x old, new, v old, new
   __shared__ uint2 phase[D / 2];
@@ -253,8 +253,16 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     ids[tid] = id;
   }
   P8 piece;
+  int arow[P8::kRuns], afrom[P8::kRuns];  // a run's angles: afrom + arow * row
   if constexpr (TURN != kTurnNone) {
     const int pairs = A.rot.pairs;
+    if (tid < 4) {
+      ct[R * pstride + tid] = 1.f;
+      st[R * pstride + tid] = -0.f;
+    }
+    // the padding of rows of x: zeros, the partners of what is not turned
+    for (int r = tid; r < kBuf * R; r += 256)
+      *reinterpret_cast<uint4*>(tiles + ((r / R) * 2 * R + r % R) * kStride + D) = make_uint4(0, 0, 0, 0);
     if (tid < pairs) {
       phase[tid] = rot_phase(A.freqs[tid]);
       axis[tid] = (uint8_t)rot_axis(A.rot, tid);
@@ -266,7 +274,13 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       for (int p = lane; p < pairs; p += 32)
         rot_angle<true>(pos[axis[p] * A.pos_axis + r], phase[p], &ct[r * pstride + p],
                         &st[r * pstride + p]);
-    piece.place(A.rot, dim0);
+    piece.place(A.rot, dim0, D);
+#pragma unroll
+    for (int q = 0; q < P8::kRuns; ++q) {
+      const bool turned = piece.turned >> (q * W) & 1;
+      arow[q] = turned ? pstride : 0;
+      afrom[q] = turned ? piece.pair[q] : R * pstride;
+    }
   }
   const int pmask = C.P - 1, pshift = __ffs(C.P) - 1, off0 = (int)base & pmask;  // off0: row 0's slot
 
@@ -306,8 +320,8 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
 #pragma unroll
           for (int q = 0; q < P8::kRuns; ++q) {
             load_w<bf16, W>(row + piece.other[q], &y[q * W]);
-            load_w<float, W>(ct + r * pstride + piece.pair[q], &c[q * W]);
-            load_w<float, W>(st + r * pstride + piece.pair[q], &s[q * W]);
+            load_w<float, W>(ct + afrom[q] + r * arow[q], &c[q * W]);
+            load_w<float, W>(st + afrom[q] + r * arow[q], &s[q * W]);
 #pragma unroll
             for (int e = 0; e < W; ++e) s[q * W + e] *= piece.sign_of(q * W + e);
           }

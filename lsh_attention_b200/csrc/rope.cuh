@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "lsh_attn.h"
+#include "sm100.cuh"
 
 namespace lsh {
 
@@ -89,11 +90,13 @@ template <int N, int W, bool ADJ>
 struct Piece {
   static constexpr int kRuns = ADJ ? 1 : N / W;
   static constexpr int kPairs = ADJ ? N / 2 : N;  // angles
+  static constexpr uint32_t kAll = (1u << kPairs) - 1;
   int other[kRuns];       // halves: first partner dimension of each run
   int pair[kRuns];        // first pair of each run
   uint32_t first, turned;  // bit per run: first half; bit per angle: is rotated
 
-  __device__ __forceinline__ void place(const RotPlan& R, int dim0) {
+  // Runs that are not rotated find zeros as partners, at `zeros` from the row.
+  __device__ __forceinline__ void place(const RotPlan& R, int dim0, int zeros) {
     first = turned = 0;
     if constexpr (ADJ) {
       pair[0] = dim0 / 2;
@@ -104,7 +107,7 @@ struct Piece {
 #pragma unroll
       for (int k = 0; k < kRuns; ++k) {
         const int dim = dim0 + k * W;
-        other[k] = dim;
+        other[k] = zeros;
         pair[k] = 0;
         if (dim >= 2 * R.pairs) continue;
         int a = 0;
@@ -126,30 +129,40 @@ struct Piece {
     return !ADJ && (first >> (i / W) & 1) ? -1.f : 1.f;
   }
   // x: the piece; y: its partners (halves); c, s: of every angle, s signed.
-  // Spelled out, so that every kernel rounds alike; what is not turned is copied,
-  // not multiplied: it may be infinite.
+  // Spelled out, so that every kernel rounds alike. What is not turned is copied:
+  // halves with c = 1, s = -0 and zeros as partners (x + -0 is x, of any x);
+  // neighbours by leaving them out (a partner may be infinite).
   __device__ __forceinline__ void turn(float (&x)[N], const float (&y)[N], const float (&c)[kPairs],
                                        const float (&s)[kPairs]) const {
+    if constexpr (!ADJ) {
 #pragma unroll
-    for (int i = 0; i < kPairs; ++i) {
-      if (!(turned >> i & 1)) continue;
-      if constexpr (ADJ) {
-        const float lo = x[2 * i], hi = x[2 * i + 1];
-        x[2 * i] = __fmaf_rn(lo, c[i], __fmul_rn(hi, -s[i]));
-        x[2 * i + 1] = __fmaf_rn(hi, c[i], __fmul_rn(lo, s[i]));
-      } else {
-        x[i] = __fmaf_rn(x[i], c[i], __fmul_rn(y[i], s[i]));
-      }
+      for (int i = 0; i < N; ++i) x[i] = __fmaf_rn(x[i], c[i], __fmul_rn(y[i], s[i]));
+    } else if (turned == kAll) {
+      pairs<true>(x, c, s);
+    } else {
+      pairs<false>(x, c, s);
+    }
+  }
+  template <bool ALL>
+  __device__ __forceinline__ void pairs(float (&x)[N], const float (&c)[kPairs],
+                                        const float (&s)[kPairs]) const {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      if (!ALL && !(turned >> i & 1)) continue;
+      const float lo = x[2 * i], hi = x[2 * i + 1];
+      x[2 * i] = __fmaf_rn(lo, c[i], __fmul_rn(hi, -s[i]));
+      x[2 * i + 1] = __fmaf_rn(hi, c[i], __fmul_rn(lo, s[i]));
     }
   }
 };
 
-constexpr int kRopeHeads = 4;  // heads loaded together by a thread
+constexpr int kRopeHeads = 4;  // heads of a batch
 
 struct RopeArgs {
   const int32_t* pos;
   const float* freqs;
   int B, H, n;
+  int tiles;           // of a sequence's tokens
   int heads_per;       // heads a thread turns with the same sines
   int head_groups;
   int64_t pos_axis, pos_batch;  // strides of positions
@@ -158,93 +171,140 @@ struct RopeArgs {
   RotPlan rot;
 };
 
-// One thread holds a piece of a token: its sines and cosines serve every head of
-// its group, so that the angles cost a fraction 1 / heads_per of the rows. Bound
-// by DRAM: what counts is whole sectors and bytes in flight, four heads' pieces
-// a thread. Halves: the lanes of a row form each angle once and share them, and
-// pass one another their pieces, through shared memory (partners read from
-// global memory as well: 95 us instead of __ROPE_IMAGE__ us at B8 H8 n12288 d64 with axes
-// 24, 24, 16).
-// grid (blocks over tokens x pieces, batch x head groups), block 256.
+// A job is a tile of tokens (256 pieces of rows) for a group of heads; a block
+// takes one or more in turn. A thread's sines and cosines serve every head of the
+// group: the angles cost a fraction 1 / heads_per of the rows. What bounds the
+// kernel besides DRAM is the instructions beside the rotation itself: where a
+// piece lies, the phases, the angles. Rows come by cp.async, two batches of heads
+// ahead, and are under way meanwhile. Halves: the lanes of a row form each angle
+// once and find their partners' pieces in shared memory. Measured: 45 us at B1 H8
+// n65536 d128, neighbours (0.91 of the copy rate), 43 us at B8 H8 n12288 d64, axes
+// 24, 24, 16 by halves (0.72; with partners read from global memory too, 95 us).
+// grid (blocks), block 256.
 template <typename T, int D, int W, bool ADJ>
 __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
   constexpr int N = 16 / sizeof(T), kPieces = D / N;  // a row's pieces lie in one warp
   constexpr int kTok = 256 / kPieces;
-  using P = Piece<N, W, ADJ>;
   constexpr bool kFast = sizeof(T) == 2;
+  using P = Piece<N, W, ADJ>;
   __shared__ float ct[ADJ ? 1 : kTok * D / 2], st[ADJ ? 1 : kTok * D / 2];
+  __shared__ uint4 rows[2][kRopeHeads][257];  // a batch of heads each; the last piece: zeros
   __shared__ uint2 phase[D / 2];
   __shared__ uint8_t axis[D / 2];
-  __shared__ uint4 swap[ADJ ? 1 : kRopeHeads][256];
-  const int64_t tok0 = (int64_t)blockIdx.x * kTok;
   const int tl = threadIdx.x / kPieces, dim0 = threadIdx.x % kPieces * N;
-  const int64_t tok = tok0 + tl;
-  const bool in = tok < A.n;
   const int pairs = A.rot.pairs;
+  const int batches = (A.heads_per + kRopeHeads - 1) / kRopeHeads;
+
+  struct Job {
+    int tile, group, b;
+  };
+  auto next = [&](Job& j, int step) {
+    j.tile += step;
+    while (j.tile >= A.tiles) {
+      j.tile -= A.tiles;
+      if (++j.group == A.head_groups) {
+        j.group = 0;
+        ++j.b;
+      }
+    }
+  };
+  // batches of heads, numbered through the block's jobs, two under way
+  Job ahead{0, 0, 0};
+  next(ahead, blockIdx.x);
+  Job job = ahead;
+  int batch_f = 0, buf = 0;
+  auto fetch = [&](int to) {
+    if (ahead.b < A.B) {
+      const int h = ahead.group * A.heads_per + batch_f * kRopeHeads;
+      const int n = min((ahead.group + 1) * A.heads_per, A.H) - h;
+      const int64_t tok = (int64_t)ahead.tile * kTok + tl;
+      const T* xp = x + ahead.b * A.xs[0] + h * A.xs[1] + tok * A.xs[2] + dim0;
+      if (tok < A.n) {
+#pragma unroll
+        for (int k = 0; k < kRopeHeads; ++k, xp += A.xs[1])
+          if (k < n) sm100::cp_async16_zfill(&rows[to][k][threadIdx.x], xp, true);
+      }
+      if (++batch_f == batches) {
+        batch_f = 0;
+        next(ahead, gridDim.x);
+      }
+    }
+    sm100::cp_async_commit();
+  };
+  fetch(0);
+  fetch(1);
   if (threadIdx.x < pairs) {
     phase[threadIdx.x] = rot_phase(A.freqs[threadIdx.x]);
     axis[threadIdx.x] = (uint8_t)rot_axis(A.rot, threadIdx.x);
   }
-  __syncthreads();
+  if (!ADJ && threadIdx.x < 2 * kRopeHeads)
+    rows[threadIdx.x / kRopeHeads][threadIdx.x % kRopeHeads][256] = make_uint4(0, 0, 0, 0);
   P piece;
-  piece.place(A.rot, dim0);
-  for (int64_t bg = blockIdx.y; bg < (int64_t)A.B * A.head_groups; bg += gridDim.y) {
-    const int b = (int)(bg / A.head_groups), h0 = (int)(bg % A.head_groups) * A.heads_per;
-    const int h1 = min(h0 + A.heads_per, A.H);
-    const T* xp = x + b * A.xs[0] + (in ? tok : 0) * A.xs[2] + dim0;
-    T* op = out + b * A.os[0] + tok * A.os[2] + dim0;
-    const int32_t* pos = A.pos + b * A.pos_batch;
+  piece.place(A.rot, dim0, (256 - tl * kPieces) * N);
+  // a thread's first angle of a tile's, and its stride: no division in the loop
+  const int first_tok = threadIdx.x / pairs, first_pair = threadIdx.x % pairs;
+  const int step_tok = 256 / pairs, step_pair = 256 % pairs;
+  float sign[P::kPairs];
+#pragma unroll
+  for (int i = 0; i < P::kPairs; ++i) sign[i] = A.sign * piece.sign_of(i);
+
+  for (; job.b < A.B; next(job, gridDim.x)) {
+    const int h0 = job.group * A.heads_per, h1 = min(h0 + A.heads_per, A.H);
+    const int64_t tok0 = (int64_t)job.tile * kTok;
+    const bool in = tok0 + tl < A.n;
+    T* oh = out + job.b * A.os[0] + h0 * A.os[1] + (tok0 + tl) * A.os[2] + dim0;
+    const int32_t* pos = A.pos + job.b * A.pos_batch + tok0;
     float c[P::kPairs], s[P::kPairs];
+    __syncthreads();  // the phases are there, the angles of the job before taken
     if constexpr (!ADJ) {
-      __syncthreads();  // the angles of the batch before have been taken
       const int toks = (int)min((int64_t)kTok, A.n - tok0);
-      for (int i = threadIdx.x; i < toks * pairs; i += 256) {
-        const int p = i % pairs;
-        rot_angle<kFast>(pos[axis[p] * A.pos_axis + tok0 + i / pairs], phase[p], &ct[i], &st[i]);
+      for (int t = first_tok, p = first_pair; t < toks;) {
+        rot_angle<kFast>(pos[axis[p] * A.pos_axis + t], phase[p], &ct[t * pairs + p],
+                         &st[t * pairs + p]);
+        t += step_tok;
+        p += step_pair;
+        if (p >= pairs) {
+          p -= pairs;
+          ++t;
+        }
       }
       __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < P::kPairs; ++i) {
       c[i] = 1.f;
-      s[i] = 0.f;
+      s[i] = -0.f;
       if (in && (piece.turned >> i & 1)) {
         const int p = piece.pair_of(i);
         if constexpr (ADJ) {
-          rot_angle<kFast>(pos[axis[p] * A.pos_axis + tok], phase[p], &c[i], &s[i]);
+          rot_angle<kFast>(pos[axis[p] * A.pos_axis + tl], phase[p], &c[i], &s[i]);
         } else {
           c[i] = ct[tl * pairs + p];
           s[i] = st[tl * pairs + p];
         }
-        s[i] *= A.sign * piece.sign_of(i);
+        s[i] *= sign[i];
       }
     }
-    // heads in batches, all of a batch loaded before the first is stored (x and
-    // out may be the same rows)
-    for (int h = h0; h < h1; h += kRopeHeads) {
-      uint4 u[kRopeHeads];
+    for (int h = h0; h < h0 + batches * kRopeHeads; h += kRopeHeads) {
+      sm100::cp_async_wait_prev();
+      __syncwarp();
 #pragma unroll
-      for (int k = 0; k < kRopeHeads; ++k)
-        if (h + k < h1) u[k] = *reinterpret_cast<const uint4*>(xp + (h + k) * A.xs[1]);
-      if constexpr (!ADJ) {
-#pragma unroll
-        for (int k = 0; k < kRopeHeads; ++k) swap[k][threadIdx.x] = u[k];
-        __syncwarp();
-      }
-#pragma unroll
-      for (int k = 0; k < kRopeHeads; ++k)
-        if (h + k < h1 && in) {
+      for (int k = 0; k < kRopeHeads; ++k, oh += A.os[1])
+        if (h + k < h1) {
+          const uint4* row = &rows[buf][k][tl * kPieces];
           float f[N], y[N];
-          Vec16<T>::unpack(u[k], f);
+          Vec16<T>::unpack(rows[buf][k][threadIdx.x], f);
           if constexpr (!ADJ) {
-            const T* row = reinterpret_cast<const T*>(&swap[k][tl * kPieces]);
 #pragma unroll
-            for (int r = 0; r < P::kRuns; ++r) load_w<T, W>(row + piece.other[r], &y[r * W]);
+            for (int r = 0; r < P::kRuns; ++r)
+              load_w<T, W>(reinterpret_cast<const T*>(row) + piece.other[r], &y[r * W]);
           }
           piece.turn(f, y, c, s);
-          *reinterpret_cast<uint4*>(op + (h + k) * A.os[1]) = pack16<T>(f);
+          if (in) *reinterpret_cast<uint4*>(oh) = pack16<T>(f);
         }
-      if constexpr (!ADJ) __syncwarp();
+      __syncwarp();
+      fetch(buf);
+      buf ^= 1;
     }
   }
 }

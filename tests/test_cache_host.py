@@ -152,6 +152,7 @@ class Cache:
 
     def __init__(self, index=0):
         self.k = Tensor((4, H, 16, D), index=index)
+        self.kind = index
 
 
 def ints(*shape, index=0):
