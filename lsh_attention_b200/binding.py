@@ -530,7 +530,7 @@ def lsh_rope(x, positions, freqs, *, axis_dims, adjacent: bool = False, inverse:
     desc = _plans.get(key) or _keep(key, _plan_rope(x, positions, freqs, key[2], adjacent, inverse,
                                                     out))
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     _check((_lib or load()).lsh_rope(desc, x.data_ptr(), positions.data_ptr(), freqs.data_ptr(),
                                      out.data_ptr(), _raw_stream(x.device)))
     return out
@@ -650,7 +650,7 @@ def lsh_cache_append(cache: LshCache, x, v, page_table, seq_len, *, n_valid=None
     rows, rot = _plans.get(key) or _keep(key, _plan_append(
         cache, x, v, page_table, seq_len, n_valid, positions, freqs, key[3], adjacent, xr))
     if xr is None and axis_dims:
-        xr = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        xr = torch.empty_like(x, memory_format=torch.contiguous_format)
     _check((_lib or load()).lsh_cache_append(
         cache.desc_ref, cache.memory_ref, rows, rot, x.data_ptr(), v.data_ptr(), _opt(positions),
         _opt(freqs), page_table.data_ptr(), seq_len.data_ptr(), _opt(n_valid), _opt(xr),
@@ -732,7 +732,7 @@ def lsh_cache_attend(cache: LshCache, x, page_table, seq_len, *, n_valid=None, o
                                                             out, lse, ws))
     device = x.device
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if lse is None:
         lse = torch.empty(x.shape[:3], dtype=torch.float32, device=device)
     stream = _raw_stream(device)

@@ -57,12 +57,12 @@ __device__ __forceinline__ int64_t page_base(const CacheView& C, int id, int h) 
   return ((int64_t)id * C.H + h) * C.P * C.d;
 }
 
-// Smallest power of two s >= 2^-126 with amax <= 127 s. amax finite, >= 0.
+// Smallest power of two s >= 2^-126 with amax <= 127 s. amax finite, >= 0: with
+// amax = f 2^e, f in [1, 2), that is 2^(e - 6), or 2^(e - 5) where f > 127 / 64.
 __device__ __forceinline__ float scale_for(float amax) {
-  int e;
-  const float m = frexpf(amax, &e);  // amax = m 2^e, m in [0.5, 1) or 0
-  e = m == 0.f ? -126 : e - 7 + (m > 127.f / 128.f);
-  return ldexpf(1.f, max(e, -126));
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 6 + ((b & 0x7fffffu) > 0x7e0000u);  // biased
+  return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
 // 1 / s of a power of two s in [2^-126, 2^126].
@@ -134,8 +134,10 @@ constexpr size_t append_smem(int rows, int d, int pairs, int buffers) {
   return (size_t)rows * (buffers * 2 * (d * 2 + 16) + append_pairs(pairs) * 8) + 32 + 128;
 }
 
-// Tiles of two heads, unless 128 rows of 128 leave room for one.
+// Tiles of two heads, and four blocks an SM; 128 rows of 128 leave room for one
+// head and one block, which has more threads.
 constexpr int append_buffers(int d, int rows) { return d * rows > 128 * 64 ? 1 : 2; }
+constexpr int append_threads(int d, int rows) { return d * rows > 128 * 64 ? 1024 : 256; }
 
 // 1/||x|| of a row whose kLanes lanes hold its values by eight; of a row that is
 // not there (not `in`), anything.
@@ -166,8 +168,8 @@ __device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
 }
 
 // One block: R consecutive token slots of one sequence for a few heads. The sines
-// of its tokens are formed once and serve its heads; the next head's rows travel
-// (cp.async) while this one's are worked on. A thread takes 16-byte pieces of
+// of its tokens are formed once and serve its heads; the next two heads' rows
+// travel (cp.async) meanwhile. A thread takes 16-byte pieces of
 // rows of x: 1/||x||, the rotation with the partners from shared memory, the
 // rotated piece out. v leaves through transposed 8x8 tiles (ldmatrix), so that a
 // thread stores four tokens of a dimension together and a warp whole sectors of
@@ -175,12 +177,14 @@ __device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
 // (maxima of non-negative floats by integer atomicMax in shared memory: the same
 // whatever the order); this block alone owns the page's head, so earlier rows
 // are rounded again in place.
-// grid (blocks of rows, head groups, batch), block 256.
+// grid (blocks of rows, head groups, batch), block append_threads(D, R).
 template <int D, bool I8, int R, int TURN>
-__global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
+__global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D, R))
+    k_cache_append(AppendArgs A) {
   constexpr int kStride = D + 8;  // elements of a shared row: 16 bytes of padding
   constexpr int kPieces = D / 8;  // 16-byte pieces of a row
-  constexpr int kPass = R * kPieces / 256;
+  constexpr int kThreads = append_threads(D, R), kWarps = kThreads / 32;
+  constexpr int kPass = R * kPieces / kThreads;
   constexpr int kBuf = append_buffers(D, R);
   constexpr int W = TURN == kTurnSingles ? 1 : 4;
   constexpr bool ADJ = TURN == kTurnAdjacent;
@@ -197,7 +201,7 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     const int t0 = max(nv, (int)min((int64_t)T, (int64_t)blockIdx.x * R));
     const int t1 = (int)min((int64_t)T, (int64_t)(blockIdx.x + 1) * R);
     const int pad = max(t1 - t0, 0) * (h1 - h0) * kPieces;
-    for (int i = tid; i < pad; i += 256) {
+    for (int i = tid; i < pad; i += kThreads) {
       const int piece = i % kPieces, rest = i / kPieces;
       const int h = h0 + rest % (h1 - h0), t = t0 + rest / (h1 - h0);
       *reinterpret_cast<uint4*>(A.xr + b * A.os[0] + h * A.os[1] + t * A.os[2] + piece * 8) =
@@ -223,9 +227,10 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   __shared__ float scales[2][4];  // of a page: x old, new, v old, new
   __shared__ uint2 phase[D / 2];
   __shared__ uint8_t axis[D / 2];
+  __shared__ int32_t pos[LSH_ROPE_MAX_AXES * R];
 
-  // a thread's pieces are the same dimensions of rows 256 / kPieces apart
-  constexpr int kStep = 256 / kPieces;
+  // a thread's pieces are the same dimensions of rows kStep apart
+  constexpr int kStep = kThreads / kPieces;
   const int dim0 = tid % kPieces * 8, row0 = tid / kPieces;
   auto fetch = [&](int h) {
     bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride + row0 * kStride + dim0;
@@ -242,6 +247,7 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     sm100::cp_async_commit();
   };
   fetch(h0);
+  if (kBuf == 2 && h0 + 1 < h1) fetch(h0 + 1);
   const int pages = (R + C.P - 1) / C.P;  // a block's tokens lie in this many
   if (tid < pages) {
     // the page of the block's tokens from row tid * P on, if it has new ones
@@ -261,19 +267,22 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       st[R * pstride + tid] = -0.f;
     }
     // the padding of rows of x: zeros, the partners of what is not turned
-    for (int r = tid; r < kBuf * R; r += 256)
+    for (int r = tid; r < kBuf * R; r += kThreads)
       *reinterpret_cast<uint4*>(tiles + ((r / R) * 2 * R + r % R) * kStride + D) = make_uint4(0, 0, 0, 0);
+    // every position at once: a load for each angle would wait in turn
+    for (int i = tid; i < A.rot.axes * R; i += kThreads) {
+      const int r = i % R;
+      if (r >= r0 && r < r1) pos[i] = A.pos[(i / R) * A.pos_axis + b * A.pos_batch + tok0 + r];
+    }
     if (tid < pairs) {
       phase[tid] = rot_phase(A.freqs[tid]);
       axis[tid] = (uint8_t)rot_axis(A.rot, tid);
     }
     __syncthreads();
-    const int32_t* pos = A.pos + b * A.pos_batch + tok0;
     // rows go round a warp at a time: lanes take neighbouring pairs
-    for (int r = r0 + warp; r < r1; r += 8)
+    for (int r = r0 + warp; r < r1; r += kWarps)
       for (int p = lane; p < pairs; p += 32)
-        rot_angle<true>(pos[axis[p] * A.pos_axis + r], phase[p], &ct[r * pstride + p],
-                        &st[r * pstride + p]);
+        rot_angle<true>(pos[axis[p] * R + r], phase[p], &ct[r * pstride + p], &st[r * pstride + p]);
     piece.place(A.rot, dim0, D);
 #pragma unroll
     for (int q = 0; q < P8::kRuns; ++q) {
@@ -285,12 +294,8 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
   const int pmask = C.P - 1, pshift = __ffs(C.P) - 1, off0 = (int)base & pmask;  // off0: row 0's slot
 
   for (int h = h0; h < h1; ++h) {
-    if (kBuf == 2 && h + 1 < h1) {
-      fetch(h + 1);
-      sm100::cp_async_wait_prev();
-    } else {
-      sm100::cp_async_wait_all();
-    }
+    if (kBuf == 2 && h + 1 < h1) sm100::cp_async_wait_prev();
+    else sm100::cp_async_wait_all();
     if (I8 && tid < 4) amax[tid] = 0;
     __syncthreads();
     const bf16* xt = tiles + ((h - h0) % kBuf) * 2 * R * kStride;
@@ -302,6 +307,7 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     for (int k = 0; k < kPass; ++k) {
       const int r = row0 + k * kStep;
       const bool in = r >= r0 && r < r1;
+      if (!__any_sync(~0u, in)) continue;
       const bf16* row = xt + r * kStride;
       float f[8];
       uint4 u = *reinterpret_cast<const uint4*>(row + dim0);
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       if (old > 0 && id >= 0 && scales[pf][1] != scales[pf][0]) {
         int8_t* kp = static_cast<int8_t*>(C.k) + page_base(C, id, h);
         const float f = scales[pf][0] / scales[pf][1];  // a power of two
-        for (int i = tid; i < old * D / 4; i += 256) {
+        for (int i = tid; i < old * D / 4; i += kThreads) {
           char4 q = *reinterpret_cast<char4*>(kp + 4 * i);
           q.x = (signed char)rintf(q.x * f);
           q.y = (signed char)rintf(q.y * f);
@@ -416,7 +422,7 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
     // v: warps take (group of 16 tokens, 16 dimensions) in turn
     constexpr int kSteps = D / 16;
     const int g0 = again ? r0 / C.P * C.P / kGroup : r0 / kGroup, g1 = (r1 - 1) / kGroup;
-    for (int w = warp; w < (g1 - g0 + 1) * kSteps; w += 8) {
+    for (int w = warp; w < (g1 - g0 + 1) * kSteps; w += kWarps) {
       const int rb = (g0 + w / kSteps) * kGroup, d0 = (w % kSteps) * 16;
       // tiles 0, 1: tokens {0,1,4,5,8,9,12,13} and {2,3,6,7,10,11,14,15} of
       // dimensions d0 ..; tiles 2, 3 the same of the next eight: lane (g, t) then
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(256) k_cache_append(AppendArgs A) {
       }
     }
     __syncthreads();  // the tile is free
-    if (kBuf == 1 && h + 1 < h1) fetch(h + 1);
+    if (h + kBuf < h1) fetch(h + kBuf);
   }
 }
 

@@ -155,7 +155,7 @@ lsh_status launch_append_t(const AppendArgs& A, cudaStream_t st) {
   if (!allow_smem(kern, (int)append_smem(R, D, D / 2, kBuf), &done)) return LSH_ERR_CUDA;
   const dim3 grid((unsigned)((A.S.n + R - 2) / R + 1),
                   (unsigned)((A.C.H + A.heads_per - 1) / A.heads_per), (unsigned)A.S.B);
-  kern<<<grid, 256, append_smem(R, D, A.rot.pairs, kBuf), st>>>(A);
+  kern<<<grid, append_threads(D, R), append_smem(R, D, A.rot.pairs, kBuf), st>>>(A);
   return last_cuda();
 }
 
@@ -299,7 +299,10 @@ lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
   const bool i8 = desc->format == LSH_CACHE_I8;
   const int rows_per = append_rows(i8, A.C.P);
   const int64_t blocks = (int64_t)((A.S.n + rows_per - 2) / rows_per + 1) * A.S.B;
-  const int64_t want = 16 * sm_count();
+  // heads are split over blocks until these fill the card twice: every block forms
+  // its tokens' angles again
+  const int threads = append_threads(A.C.d, rows_per);
+  const int64_t want = 2 * (1024 / threads) * sm_count();
   const int groups = (int)std::min<int64_t>(A.C.H, std::max<int64_t>(1, want / blocks));
   A.heads_per = (A.C.H + groups - 1) / groups;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
   __shared__ uint4 rows[2][kRopeHeads][257];  // a batch of heads each; the last piece: zeros
   __shared__ uint2 phase[D / 2];
   __shared__ uint8_t axis[D / 2];
+  __shared__ int32_t pos[LSH_ROPE_MAX_AXES * kTok];
   const int tl = threadIdx.x / kPieces, dim0 = threadIdx.x % kPieces * N;
   const int pairs = A.rot.pairs;
   const int batches = (A.heads_per + kRopeHeads - 1) / kRopeHeads;
@@ -244,22 +245,35 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
   // a thread's first angle of a tile's, and its stride: no division in the loop
   const int first_tok = threadIdx.x / pairs, first_pair = threadIdx.x % pairs;
   const int step_tok = 256 / pairs, step_pair = 256 % pairs;
+  // a job's positions, fetched while the one before it is worked on
+  int32_t ahead_pos = 0;
+  auto fetch_pos = [&](const Job& j) {
+    const int a = threadIdx.x / kTok, t = threadIdx.x % kTok;
+    const int64_t tok = (int64_t)j.tile * kTok + t;
+    if (j.b < A.B && a < A.rot.axes && tok < A.n)
+      ahead_pos = A.pos[a * A.pos_axis + j.b * A.pos_batch + tok];
+  };
+  fetch_pos(job);
   float sign[P::kPairs];
 #pragma unroll
   for (int i = 0; i < P::kPairs; ++i) sign[i] = A.sign * piece.sign_of(i);
 
-  for (; job.b < A.B; next(job, gridDim.x)) {
+  while (job.b < A.B) {
     const int h0 = job.group * A.heads_per, h1 = min(h0 + A.heads_per, A.H);
     const int64_t tok0 = (int64_t)job.tile * kTok;
     const bool in = tok0 + tl < A.n;
     T* oh = out + job.b * A.os[0] + h0 * A.os[1] + (tok0 + tl) * A.os[2] + dim0;
-    const int32_t* pos = A.pos + job.b * A.pos_batch + tok0;
     float c[P::kPairs], s[P::kPairs];
-    __syncthreads();  // the phases are there, the angles of the job before taken
+    // (the angles of the job before have been taken: the barrier behind them)
+    if (threadIdx.x < LSH_ROPE_MAX_AXES * kTok) pos[threadIdx.x] = ahead_pos;
+    __syncthreads();
+    Job after = job;
+    next(after, gridDim.x);
+    fetch_pos(after);
     if constexpr (!ADJ) {
       const int toks = (int)min((int64_t)kTok, A.n - tok0);
       for (int t = first_tok, p = first_pair; t < toks;) {
-        rot_angle<kFast>(pos[axis[p] * A.pos_axis + t], phase[p], &ct[t * pairs + p],
+        rot_angle<kFast>(pos[axis[p] * kTok + t], phase[p], &ct[t * pairs + p],
                          &st[t * pairs + p]);
         t += step_tok;
         p += step_pair;
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
       if (in && (piece.turned >> i & 1)) {
         const int p = piece.pair_of(i);
         if constexpr (ADJ) {
-          rot_angle<kFast>(pos[axis[p] * A.pos_axis + tl], phase[p], &c[i], &s[i]);
+          rot_angle<kFast>(pos[axis[p] * kTok + tl], phase[p], &c[i], &s[i]);
         } else {
           c[i] = ct[tl * pairs + p];
           s[i] = st[tl * pairs + p];
@@ -285,6 +299,8 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
         s[i] *= sign[i];
       }
     }
+    __syncthreads();  // positions and angles have been taken
+    job = after;
     for (int h = h0; h < h0 + batches * kRopeHeads; h += kRopeHeads) {
       sm100::cp_async_wait_prev();
       __syncwarp();
