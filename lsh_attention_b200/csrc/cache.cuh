@@ -70,17 +70,17 @@ __device__ __forceinline__ float recip2(float s) {
   return __uint_as_float(0x7f000000u - __float_as_uint(s));
 }
 
-// x / s rounded to the nearest integer (ties to even) in [-127, 127], NaN to 0, in
-// the low byte. rs = 1 / s is a power of two, so the product is exact; adding
-// 1.5 2^23 rounds it and leaves it in the mantissa (a conversion instruction has a
-// quarter of the rate).
-__device__ __forceinline__ uint32_t quant(float x, float rs) {
-  const float v = x == x ? fminf(fmaxf(x * rs, -127.f), 127.f) : 0.f;
-  return __float_as_uint(v + 12582912.f);
+// x / s rounded to the nearest integer (ties to even), in the low byte. rs = 1 / s
+// is a power of two, so the product is exact; 1.5 2^23 added in the same
+// instruction rounds it and leaves it in the mantissa. `odd`: x may be infinite or
+// NaN: kept in [-127, 127], NaN to 0 (finite ones are, by the choice of s).
+__device__ __forceinline__ uint32_t quant(float x, float rs, bool odd) {
+  if (odd) x = x == x ? fminf(fmaxf(x, -127.f * recip2(rs)), 127.f * recip2(rs)) : 0.f;
+  return __float_as_uint(fmaf(x, rs, 12582912.f));
 }
-__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float rs) {
-  return __byte_perm(__byte_perm(quant(a, rs), quant(b, rs), 0x0040),
-                     __byte_perm(quant(c, rs), quant(d, rs), 0x0040), 0x5410);
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float rs, bool odd) {
+  return __byte_perm(__byte_perm(quant(a, rs, odd), quant(b, rs, odd), 0x0040),
+                     __byte_perm(quant(c, rs, odd), quant(d, rs, odd), 0x0040), 0x5410);
 }
 
 // Four int8 times s, a power of two, as bf16 (exact): each byte is put into the
@@ -123,10 +123,12 @@ struct AppendArgs {
 // How the rows are turned.
 enum { kTurnNone = 0, kTurnAdjacent = 1, kTurnRuns = 2, kTurnSingles = 3 };
 
-// Tokens a block covers (aligned in the sequence). bf16 tokens do not depend on
-// one another; int8 ones share their page's scale, so a block has whole pages.
-__host__ __device__ constexpr int append_rows(bool i8, int page) {
-  return !i8 || page < 32 ? 32 : page;
+// Rows that a block has room for. bf16 tokens do not depend on one another: blocks
+// of 32, aligned in the sequence. int8 ones share their page's scale, so a block
+// has whole pages, 32 or more tokens; of larger pages into which a call can put no
+// more than 17 rows, it has 32 rows from the group of the first new one on.
+__host__ __device__ constexpr int append_rows(bool i8, int page, int n) {
+  return !i8 || page < 32 || n <= 17 ? 32 : page;
 }
 // Angles of a row in shared memory, rounded up to whole float4.
 __host__ __device__ constexpr int append_pairs(int pairs) { return (pairs + 3) / 4 * 4; }
@@ -137,7 +139,9 @@ constexpr size_t append_smem(int rows, int d, int pairs, int buffers) {
 // Tiles of two heads, and four blocks an SM; 128 rows of 128 leave room for one
 // head and one block, which has more threads.
 constexpr int append_buffers(int d, int rows) { return d * rows > 128 * 64 ? 1 : 2; }
-constexpr int append_threads(int d, int rows) { return d * rows > 128 * 64 ? 1024 : 256; }
+constexpr int append_threads(int d, int rows) {
+  return d * rows > 128 * 64 ? 1024 : d * rows > 64 * 64 ? 512 : 256;
+}
 
 // 1/||x|| of a row whose kLanes lanes hold its values by eight; of a row that is
 // not there (not `in`), anything.
@@ -210,7 +214,9 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
   }
 
   // the block's slots: positions base .. base + R - 1; new rows [r0, r1) of them
-  const int64_t base = (int64_t)(len / R + blockIdx.x) * R;
+  const int span = I8 && C.P > R ? C.P : R;  // tokens between blocks
+  int64_t base = (int64_t)(len / span + blockIdx.x) * span;
+  if (span > R) base += max((int64_t)0, len - base) & ~(kGroup - 1);
   const int r0 = (int)max((int64_t)0, len - base);
   const int r1 = (int)max((int64_t)0, min((int64_t)R, (int64_t)len + nv - base));
   if (r0 >= r1) return;
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
   };
   fetch(h0);
   if (kBuf == 2 && h0 + 1 < h1) fetch(h0 + 1);
-  const int pages = (R + C.P - 1) / C.P;  // a block's tokens lie in this many
+  const int pages = (R + C.P - 1) / C.P;  // a block's rows lie in this many
   if (tid < pages) {
     // the page of the block's tokens from row tid * P on, if it has new ones
     int id = -1;
@@ -291,7 +297,9 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
       afrom[q] = turned ? piece.pair[q] : R * pstride;
     }
   }
-  const int pmask = C.P - 1, pshift = __ffs(C.P) - 1, off0 = (int)base & pmask;  // off0: row 0's slot
+  const int pmask = C.P - 1, pshift = __ffs(C.P) - 1;
+  const int off0 = (int)base & pmask;  // row 0's slot: not 0 in a larger page only
+  const int pf = r0 >> pshift, old = (off0 + r0) & pmask;  // the page of row r0, and its earlier rows
 
   for (int h = h0; h < h1; ++h) {
     if (kBuf == 2 && h + 1 < h1) sm100::cp_async_wait_prev();
@@ -302,6 +310,7 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
     const bf16* vt = xt + R * kStride;
     bf16* xo = A.xr ? A.xr + b * A.os[0] + h * A.os[1] + (int64_t)(tok0 + row0) * A.os[2] + dim0 : nullptr;
 
+    bool odd = false;  // int8: some value is not finite
     uint4 kept[I8 ? kPass : 1];
 #pragma unroll
     for (int k = 0; k < kPass; ++k) {
@@ -351,6 +360,7 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
         km = max(km & 0xffffu, km >> 16);
         vm = max(vm & 0xffffu, vm >> 16);
         if (in && max(km, vm) > 0x7f7fu) {
+          odd = true;
           cache_error(C);
           km = vm = 0;
 #pragma unroll
@@ -373,17 +383,15 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
       }
     }
 
-    bool again = false;  // int8: some page's earlier rows are rounded again
+    bool again = false;  // int8: values of the page's earlier rows are rounded again
     if constexpr (I8) {
-      __syncthreads();
+      odd = __syncthreads_or(odd);
       if (tid < 2 * pages) {
-        // rows before r0 belong to the block's first new page at most, and are
-        // old ones of the page if it starts before them
         const int pg = tid >> 1, id = ids[pg];
         float was = 0.f, now = 0x1p-126f;
         if (id >= 0) {
           float* sc = (tid & 1 ? C.vscale : C.kscale) + (int64_t)id * C.H + h;
-          if (r0 > pg * C.P) was = *sc;
+          if (pg == pf && old > 0) was = *sc;
           now = fmaxf(was, scale_for(__int_as_float(amax[tid])));
           if (now != was) *sc = now;
         }
@@ -391,20 +399,26 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
         scales[pg][2 * (tid & 1) + 1] = now;
       }
       __syncthreads();
-      const int pf = r0 / C.P;  // the page that may have earlier rows
-      const int old = r0 - pf * C.P, id = ids[pf];
-      again = old > 0 && id >= 0 && scales[pf][3] != scales[pf][2];
-      if (old > 0 && id >= 0 && scales[pf][1] != scales[pf][0]) {
-        int8_t* kp = static_cast<int8_t*>(C.k) + page_base(C, id, h);
-        const float f = scales[pf][0] / scales[pf][1];  // a power of two
-        for (int i = tid; i < old * D / 4; i += kThreads) {
-          char4 q = *reinterpret_cast<char4*>(kp + 4 * i);
-          q.x = (signed char)rintf(q.x * f);
-          q.y = (signed char)rintf(q.y * f);
-          q.z = (signed char)rintf(q.z * f);
-          q.w = (signed char)rintf(q.w * f);
-          *reinterpret_cast<char4*>(kp + 4 * i) = q;
-        }
+      // the page's earlier rows at raised scales (ratios are powers of two): all of
+      // x, of v the groups that have no new ones
+      if (old > 0 && ids[pf] >= 0) {
+        const int64_t from = page_base(C, ids[pf], h);
+        auto redo = [&](int8_t* at, int words, float f) {
+          for (int i = tid; i < words; i += kThreads) {
+            char4 q = *reinterpret_cast<char4*>(at + 4 * i);
+            q.x = (signed char)rintf(q.x * f);
+            q.y = (signed char)rintf(q.y * f);
+            q.z = (signed char)rintf(q.z * f);
+            q.w = (signed char)rintf(q.w * f);
+            *reinterpret_cast<char4*>(at + 4 * i) = q;
+          }
+        };
+        if (scales[pf][1] != scales[pf][0])
+          redo(static_cast<int8_t*>(C.k) + from, old * D / 4, scales[pf][0] * recip2(scales[pf][1]));
+        again = scales[pf][3] != scales[pf][2];
+        if (again)
+          redo(static_cast<int8_t*>(C.v) + from, old / kGroup * kGroup * D / 4,
+               scales[pf][2] * recip2(scales[pf][3]));
       }
 #pragma unroll
       for (int k = 0; k < kPass; ++k) {
@@ -415,13 +429,13 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
         Vec16<bf16>::unpack(kept[k], f);
         const int64_t at = ((int64_t)id * C.H + h) * C.P + ((off0 + r) & pmask);
         *reinterpret_cast<uint2*>(static_cast<int8_t*>(C.k) + at * D + dim0) =
-            make_uint2(quant4(f[0], f[1], f[2], f[3], rs), quant4(f[4], f[5], f[6], f[7], rs));
+            make_uint2(quant4(f[0], f[1], f[2], f[3], rs, odd), quant4(f[4], f[5], f[6], f[7], rs, odd));
       }
     }
 
     // v: warps take (group of 16 tokens, 16 dimensions) in turn
     constexpr int kSteps = D / 16;
-    const int g0 = again ? r0 / C.P * C.P / kGroup : r0 / kGroup, g1 = (r1 - 1) / kGroup;
+    const int g0 = r0 / kGroup, g1 = (r1 - 1) / kGroup;
     for (int w = warp; w < (g1 - g0 + 1) * kSteps; w += kWarps) {
       const int rb = (g0 + w / kSteps) * kGroup, d0 = (w % kSteps) * 16;
       // tiles 0, 1: tokens {0,1,4,5,8,9,12,13} and {2,3,6,7,10,11,14,15} of
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
 #pragma unroll
         for (int k = 0; k < 2; ++k, dst += 8 * kGroup) {
           const uint32_t fresh = quant4(bf_lo(m[2 * k]), bf_hi(m[2 * k]), bf_lo(m[2 * k + 1]),
-                                        bf_hi(m[2 * k + 1]), rs);
+                                        bf_hi(m[2 * k + 1]), rs, odd);
           if (all) {
             *reinterpret_cast<uint32_t*>(dst) = fresh;
             continue;

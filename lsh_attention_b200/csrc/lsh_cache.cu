@@ -153,7 +153,8 @@ lsh_status launch_append_t(const AppendArgs& A, cudaStream_t st) {
   auto kern = k_cache_append<D, I8, R, TURN>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, (int)append_smem(R, D, D / 2, kBuf), &done)) return LSH_ERR_CUDA;
-  const dim3 grid((unsigned)((A.S.n + R - 2) / R + 1),
+  const int span = I8 && A.C.P > R ? A.C.P : R;  // tokens between blocks
+  const dim3 grid((unsigned)((A.S.n + span - 2) / span + 1),
                   (unsigned)((A.C.H + A.heads_per - 1) / A.heads_per), (unsigned)A.S.B);
   kern<<<grid, append_threads(D, R), append_smem(R, D, A.rot.pairs, kBuf), st>>>(A);
   return last_cuda();
@@ -169,8 +170,8 @@ lsh_status launch_append_r(const AppendArgs& A, cudaStream_t st) {
 
 template <int D>
 lsh_status launch_append(const AppendArgs& A, bool i8, cudaStream_t st) {
-  if (!i8) return launch_append_r<D, false, append_rows(false, 0)>(A, st);
-  switch (append_rows(true, A.C.P)) {
+  if (!i8) return launch_append_r<D, false, append_rows(false, 0, 0)>(A, st);
+  switch (append_rows(true, A.C.P, A.S.n)) {
     case 32: return launch_append_r<D, true, 32>(A, st);
     case 64: return launch_append_r<D, true, 64>(A, st);
     default: return launch_append_r<D, true, 128>(A, st);
@@ -297,8 +298,8 @@ lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
     A.os[i] = rows->out_stride[i];
   }
   const bool i8 = desc->format == LSH_CACHE_I8;
-  const int rows_per = append_rows(i8, A.C.P);
-  const int64_t blocks = (int64_t)((A.S.n + rows_per - 2) / rows_per + 1) * A.S.B;
+  const int rows_per = append_rows(i8, A.C.P, A.S.n), span = i8 ? std::max(A.C.P, rows_per) : rows_per;
+  const int64_t blocks = (int64_t)((A.S.n + span - 2) / span + 1) * A.S.B;
   // heads are split over blocks until these fill the card twice: every block forms
   // its tokens' angles again
   const int threads = append_threads(A.C.d, rows_per);
