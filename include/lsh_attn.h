@@ -321,7 +321,9 @@ lsh_status lsh_topk_forward(const lsh_topk_desc *desc, const void *x, const void
  *     16-byte aligned and strides multiples of 16 bytes, so both
  *     [B][H][n][d] and the projections' [B][n][H][d] are read in place.
  *     Strides of inputs may be 0 (one row for all); written rows must not
- *     overlap (LSH_ERR_INVALID_ARG). n rows per sequence are at most 2^20.
+ *     overlap (LSH_ERR_INVALID_ARG). Limits (else LSH_ERR_UNSUPPORTED): n, the
+ *     rows of a sequence, and the batch of lsh_rope 2^24; heads and the
+ *     batches of the cache's calls 65535; max_pages * page_size 2^31 - 2^24.
  *   - Lengths, page numbers and positions are read on the device: a captured
  *     graph may be replayed after they change.
  *   - Nothing is allocated and no call synchronises.

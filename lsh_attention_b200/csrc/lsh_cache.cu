@@ -45,7 +45,8 @@ bool rows_apart(const int64_t (&s)[3], int B, int H, int n, int d) {
   return true;
 }
 
-constexpr int kMaxRows = 1 << 20;
+constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxBatch = 1 << 24;
 
 // Checks `rot` and fills the plan. 0: no rotation is asked for.
 lsh_status check_rot(const lsh_rope_axes* rot, int d, RotPlan* R) {
@@ -101,7 +102,11 @@ lsh_status launch_rope(RopeArgs A, const void* x, void* out, cudaStream_t st) {
   // persistent blocks (0.72 at B8 H8 n12288 d64, axes 24, 24, 16; a job a block 0.61).
   const int64_t jobs = tiles * A.head_groups;
   const int64_t most = A.rot.adjacent ? INT32_MAX : 5 * sm_count();
-  kern<<<(unsigned)std::min(jobs, most), 256, 0, st>>>(
+  const int64_t blocks = std::min(jobs, most), rest = blocks / A.tiles;
+  A.step_tile = (int)(blocks % A.tiles);
+  A.step_group = (int)(rest % A.head_groups);
+  A.step_b = (int)(rest / A.head_groups);
+  kern<<<(unsigned)blocks, 256, 0, st>>>(
       static_cast<const T*>(x), static_cast<T*>(out), A);
   return last_cuda();
 }
@@ -134,6 +139,8 @@ lsh_status check_cache(const lsh_cache_desc* c, const lsh_cache* m, const lsh_ca
                                       c->page_size != 64 && c->page_size != 128))
     return LSH_ERR_UNSUPPORTED;
   if (r->batch > 65535 || c->heads > 65535 || r->n > kMaxRows) return LSH_ERR_UNSUPPORTED;
+  // positions are 32-bit, with the rows of a call behind them
+  if ((int64_t)r->max_pages * c->page_size > INT32_MAX - kMaxRows) return LSH_ERR_UNSUPPORTED;
   if (!m) return LSH_OK;  // sizes only
   if (!m->k || !m->v || !m->key_inv_norm || !table || !len) return LSH_ERR_INVALID_ARG;
   if (c->format == LSH_CACHE_I8 && (!m->k_scale || !m->v_scale)) return LSH_ERR_INVALID_ARG;
@@ -239,7 +246,8 @@ lsh_status lsh_rope(const lsh_rope_desc* desc, const void* x, const int32_t* pos
       (q.pos_batched != 0 && q.pos_batched != 1) ||
       (q.dtype != LSH_F32 && q.dtype != LSH_BF16) || q.rot.axes < 1)
     return LSH_ERR_INVALID_ARG;
-  if (q.d != 64 && q.d != 128) return LSH_ERR_UNSUPPORTED;
+  if ((q.d != 64 && q.d != 128) || q.n > kMaxRows || q.batch > kMaxBatch || q.heads > 65535)
+    return LSH_ERR_UNSUPPORTED;
   RopeArgs A;
   lsh_status s = check_rot(&q.rot, q.d, &A.rot);
   if (s != LSH_OK) return s;

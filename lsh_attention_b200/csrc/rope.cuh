@@ -165,6 +165,7 @@ struct RopeArgs {
   int tiles;           // of a sequence's tokens
   int heads_per;       // heads a thread turns with the same sines
   int head_groups;
+  int step_tile, step_group, step_b;  // gridDim.x jobs
   int64_t pos_axis, pos_batch;  // strides of positions
   int64_t xs[3], os[3];
   float sign;          // -1: the inverse rotation
@@ -178,11 +179,12 @@ struct RopeArgs {
 // piece lies, the phases, the angles. Rows come by cp.async, two batches of heads
 // ahead, and are under way meanwhile. Halves: the lanes of a row form each angle
 // once and find their partners' pieces in shared memory. Measured: 45 us at B1 H8
-// n65536 d128, neighbours (0.91 of the copy rate), 43 us at B8 H8 n12288 d64, axes
-// 24, 24, 16 by halves (0.72; with partners read from global memory too, 95 us).
+// n65536 d128, neighbours (0.91 of the copy rate), 39 us at B8 H8 n12288 d64, axes
+// 24, 24, 16 by halves (0.79; with partners read from global memory too, 95 us; a
+// position fetched for each angle when it is formed, 43 us).
 // grid (blocks), block 256.
 template <typename T, int D, int W, bool ADJ>
-__global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
+__global__ void __launch_bounds__(256, ADJ || W < 4 ? 1 : 5) k_rope(const T* x, T* out, RopeArgs A) {
   constexpr int N = 16 / sizeof(T), kPieces = D / N;  // a row's pieces lie in one warp
   constexpr int kTok = 256 / kPieces;
   constexpr bool kFast = sizeof(T) == 2;
@@ -196,22 +198,30 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
   const int pairs = A.rot.pairs;
   const int batches = (A.heads_per + kRopeHeads - 1) / kRopeHeads;
 
+  // jobs are numbered through tiles, head groups and sequences
   struct Job {
     int tile, group, b;
   };
-  auto next = [&](Job& j, int step) {
-    j.tile += step;
-    while (j.tile >= A.tiles) {
+  auto job_of = [&](uint32_t i) {
+    const uint32_t rest = i / (uint32_t)A.tiles;
+    return Job{(int)(i - rest * A.tiles), (int)(rest % (uint32_t)A.head_groups),
+               (int)(rest / (uint32_t)A.head_groups)};
+  };
+  auto next = [&](Job& j) {  // the job gridDim.x on: digit by digit
+    j.tile += A.step_tile;
+    j.group += A.step_group;
+    j.b += A.step_b;
+    if (j.tile >= A.tiles) {
       j.tile -= A.tiles;
-      if (++j.group == A.head_groups) {
-        j.group = 0;
-        ++j.b;
-      }
+      ++j.group;
+    }
+    if (j.group >= A.head_groups) {
+      j.group -= A.head_groups;
+      ++j.b;
     }
   };
   // batches of heads, numbered through the block's jobs, two under way
-  Job ahead{0, 0, 0};
-  next(ahead, blockIdx.x);
+  Job ahead = job_of(blockIdx.x);
   Job job = ahead;
   int batch_f = 0, buf = 0;
   auto fetch = [&](int to) {
@@ -227,7 +237,7 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
       }
       if (++batch_f == batches) {
         batch_f = 0;
-        next(ahead, gridDim.x);
+        next(ahead);
       }
     }
     sm100::cp_async_commit();
@@ -268,7 +278,7 @@ __global__ void __launch_bounds__(256) k_rope(const T* x, T* out, RopeArgs A) {
     if (threadIdx.x < LSH_ROPE_MAX_AXES * kTok) pos[threadIdx.x] = ahead_pos;
     __syncthreads();
     Job after = job;
-    next(after, gridDim.x);
+    next(after);
     fetch_pos(after);
     if constexpr (!ADJ) {
       const int toks = (int)min((int64_t)kTok, A.n - tok0);

@@ -40,6 +40,7 @@ def rope(lib, x=P, pos=P, freqs=P, out=P, rot=None, xs=HEADS_FIRST, os_=HEADS_FI
 
 @pytest.mark.parametrize("kw,status", [
     ({"batch": 0}, 1), ({"heads": -1}, 1), ({"n": 0}, 1), ({"d": 0}, 1), ({"d": 96}, 2),
+    ({"n": (1 << 24) + 1}, 2), ({"heads": 65536}, 2), ({"batch": (1 << 24) + 1}, 2),
     ({"inverse": 2}, 1), ({"pos_batched": 3}, 1), ({"dtype": 7}, 1),
     ({"x": None}, 1), ({"pos": None}, 1), ({"freqs": None}, 1), ({"out": None}, 1),
     ({"x": ODD}, 1), ({"out": ODD}, 1),
@@ -98,7 +99,7 @@ def attend(lib, kw):
     ({"m_k": 0}, 1), ({"m_v": 0}, 1), ({"m_key_inv_norm": 0}, 1), ({"m_k_scale": 0}, 1),
     ({"m_v_scale": 0}, 1), ({"m_k": 4100}, 1), ({"m_status": 4}, 1),
     ({"r_batch": 0}, 1), ({"r_n": 0}, 1), ({"r_max_pages": 0}, 1), ({"r_batch": 65536}, 2),
-    ({"r_n": (1 << 20) + 1}, 2), ({"r_x": (0, 0, 12)}, 1), ({"r_x": (0, -8, 8)}, 1),
+    ({"r_n": (1 << 24) + 1}, 2), ({"r_max_pages": (1 << 27) - (1 << 20)}, 2), ({"r_x": (0, 0, 12)}, 1), ({"r_x": (0, -8, 8)}, 1),
     ({"x": None}, 1), ({"x": ODD}, 1), ({"table": None}, 1), ({"len": None}, 1),
 ])
 def test_cache_refusals(lib, call, kw, status):

@@ -120,6 +120,26 @@ def test_rope_layouts(n, heads):
         lb.lsh_rope(x, pos, f, axis_dims=dims, out=base[:, :1].expand(-1, heads, -1, -1))
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("B,H,n", [(3000, 1, 1), (700, 9, 2), (2, 33, 130), (1, 1, 40000)])
+def test_rope_many_and_few_tiles(B, H, n, adjacent):
+    """More sequences, heads or tiles than blocks: every row is the one that it is alone."""
+    d, dims = 64, (40,)
+    x = randn(B, H, n, d).bfloat16().cuda()
+    pos = (torch.arange(B * n, dtype=torch.int32).view(1, B, n) % 5000).cuda()
+    f = freqs_of(dims).cuda()
+    out = lb.lsh_rope(x, pos, f, axis_dims=dims, adjacent=adjacent)
+    rows = x.transpose(1, 2).reshape(1, 1, B * n * H, d)
+    alone = lb.lsh_rope(rows, pos.view(1, -1, 1).expand(-1, -1, H).reshape(1, -1).contiguous(), f,
+                        axis_dims=dims, adjacent=adjacent)
+    assert torch.equal(out, alone.view(B, n, H, d).transpose(1, 2))
+    few = torch.randint(0, B * n, (20,), generator=torch.Generator().manual_seed(0))
+    b, t = few // n, few % n
+    got, src = out[b.cuda(), :, t.cuda()].cpu(), x[b.cuda(), :, t.cuda()].cpu()
+    want = oc.rope(src[:, :, None], pos[0, b.cuda(), t.cuda()].cpu().view(1, 20, 1), f.cpu(), dims, adjacent)
+    near(got, want[:, :, 0], rope_tol(src, dims, adjacent, 2.0 ** -8), "rows")
+
+
 def test_rope_gradient_against_differences():
     """The map is linear: the difference along any direction is the map of the direction, so the
     gradient of sum(g * rope(x)) along e is <g, rope(e)>."""
