@@ -184,7 +184,7 @@ struct RopeArgs {
 // position fetched for each angle when it is formed, 43 us).
 // grid (blocks), block 256.
 template <typename T, int D, int W, bool ADJ>
-__global__ void __launch_bounds__(256, ADJ || W < 4 ? 1 : 5) k_rope(const T* x, T* out, RopeArgs A) {
+__global__ void __launch_bounds__(256, ADJ || W < 4 ? 0 : 5) k_rope(const T* x, T* out, RopeArgs A) {
   constexpr int N = 16 / sizeof(T), kPieces = D / N;  // a row's pieces lie in one warp
   constexpr int kTok = 256 / kPieces;
   constexpr bool kFast = sizeof(T) == 2;
