@@ -449,7 +449,7 @@ lsh_status lsh_cache_attend_workspace_size(const lsh_cache_desc *desc,
  *   out bf16 (out_stride), lse [batch][heads][n] fp32, natural log.
  * Rows past n_valid, and rows that see nothing (bad pages), are zeros with
  * lse = -inf. Made for few tokens a sequence (one, or a handful of drafted
- * ones): every eight rows read the cache once. Deterministic on one device. */
+ * ones): up to sixteen rows read the cache once. Deterministic on one device. */
 lsh_status lsh_cache_attend(const lsh_cache_desc *desc, const lsh_cache *cache,
                             const lsh_cache_rows *rows, const void *x,
                             const int32_t *page_table, const int32_t *seq_len,

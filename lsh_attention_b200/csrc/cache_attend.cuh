@@ -6,8 +6,8 @@
 // With one row, or a handful, for every sequence and head, each cached byte is
 // used once: the kernel is a stream through the cache and is bound by DRAM.
 //
-// Work. A unit is 8 KB of the cache for one (sequence, head, eight rows), a
-// segment: 64 tokens (int8, d 64), 32 or 16 (bf16, d 128). Units are numbered
+// Work. A unit is 8 KB of the cache for one (sequence, head, eight or sixteen
+// rows), a segment: 64 tokens (int8, d 64), 32 or 16 (bf16, d 128). Units are numbered
 // through sequences, heads, row groups and tokens, and every computing warp of
 // the card takes an equal run of them, whatever the lengths are: they are read on
 // the device. Warps do not wait for one another. A segment that several of them
@@ -18,14 +18,15 @@
 // computing warps: four lanes walk a warp's run, look the pages of its next unit
 // up and fill its own ring of shared-memory stages by bulk copies.
 //
-// S = Q K^T and O += P V are warp products (m16n8k16): eight rows do not fill a
+// S = Q K^T and O += P V are warp products (m16n8k16): so few rows do not fill a
 // tcgen05 tile, and DRAM allows ten times the tensor work. A contraction's index
 // may be permuted at will as long as both operands agree, so a lane takes
 // dimensions of K (16 bytes) and tokens of V (four of a group of 16, which lies
 // dimension by dimension in the cache) that are consecutive in memory, and feeds
-// them to the products as they are: no transposes, no shuffles. In bf16 the 16 rows of P
-// hold the weights of eight as high and low parts, 2^-17 together, so that P V
-// loses nothing against fp32 weights.
+// them to the products as they are: no transposes, no shuffles. bf16 weights go in
+// high and low parts, 2^-17 together, so that P V loses nothing against fp32
+// ones: of eight rows in one product, whose 16 rows hold both, of sixteen (calls
+// of more than eight rows) in two.
 //
 // int8: what bounds the kernel besides DRAM is the instructions that widen the
 // bytes. A byte of K becomes the f16 subnormal (q + 128) 2^-24 by being put under
@@ -44,7 +45,6 @@
 
 namespace lsh {
 
-constexpr int kAttRows = 8;     // rows of a segment
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttendArgs {
@@ -55,8 +55,8 @@ struct AttendArgs {
   float* lse;
   int64_t xs[3], os[3];
   int groups;      // segments of a (sequence, head), most
-  float* part;     // [computing warps][2][8][D] unnormalised sums of split segments
-  float* part_ml;  // [computing warps][2][8][2] their references (log2) and weights' sums
+  float* part;     // [computing warps][2][rows][D] unnormalised sums of split segments
+  float* part_ml;  // [computing warps][2][rows][2] their references (log2) and weights' sums
   int4* rec;       // [B][H][groups]: first warp, how many share it (0: it is whole), rows
 };
 
@@ -145,9 +145,9 @@ __device__ __forceinline__ float ex2(float x) {
 
 // ------------------------------------------------------------- the copying warps
 // A sequence's row groups and units of a segment of it; all its units.
-template <int kTok>
+template <int kTok, int kRows>
 __device__ __forceinline__ int64_t att_units(int H, int len, int nv, int* groups, int* units) {
-  *groups = (nv + kAttRows - 1) / kAttRows;
+  *groups = (nv + kRows - 1) / kRows;
   *units = (int)(((int64_t)len + nv + kTok - 1) / kTok);
   return (int64_t)H * *groups * *units;
 }
@@ -172,7 +172,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 
 // Copying warp `pw`: lanes 4 q .. 4 q + 3 serve computing warp pw kWarps / 4 + q,
 // lane 4 q + s the tokens 16 s .. of its units. The lane groups go their own ways.
-template <int D, bool I8>
+template <int D, bool I8, int RG>
 __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64_t* full,
                               uint64_t* empty, int pw) {
   using Cfg = AttCfg<D, I8>;
@@ -189,7 +189,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
   auto window = [&](int base) {
     wlen = wnv = 0;
     if (base + lane < S.B) seq_rows(S, C.P, base + lane, &wlen, &wnv);
-    return att_units<Cfg::kTok>(C.H, wlen, wnv, &groups, &units);
+    return att_units<Cfg::kTok, 8 * RG>(C.H, wlen, wnv, &groups, &units);
   };
   int64_t N = 0, first_window = 0;
   for (int base = 0; base < S.B; base += 32) {
@@ -226,7 +226,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
       if (S.B > 32) {
         wlen = wnv = 0;
         if (base + lane < S.B) seq_rows(S, C.P, base + lane, &wlen, &wnv);
-        own = att_units<Cfg::kTok>(C.H, wlen, wnv, &g0, &u0);
+        own = att_units<Cfg::kTok, 8 * RG>(C.H, wlen, wnv, &g0, &u0);
       }
       int64_t incl = own;
 #pragma unroll
@@ -245,7 +245,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
           b = base + l;
           len = l_len;
           nv = l_nv;
-          att_units<Cfg::kTok>(C.H, len, nv, &groups, &units);
+          att_units<Cfg::kTok, 8 * RG>(C.H, len, nv, &groups, &units);
           const int64_t hg = udiv(at, units);
           unit = (int)(at - hg * units);
           h = (int)udiv(hg, groups);
@@ -268,7 +268,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
     k.flags = kEnd;
     k.id = -1;
     if (left == 0) return;
-    const int q0 = grp * kAttRows, rows = min(kAttRows, nv - q0);
+    const int q0 = grp * 8 * RG, rows = min(8 * RG, nv - q0);
     if (unit == 0) starts = true;
     if (starts) {
       head = unit == 0;
@@ -304,7 +304,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
           do {  // the next sequence with rows
             seq_rows(S, C.P, ++b, &len, &nv);
           } while (nv == 0);
-          att_units<Cfg::kTok>(C.H, len, nv, &groups, &units);
+          att_units<Cfg::kTok, 8 * RG>(C.H, len, nv, &groups, &units);
         }
       }
     }
@@ -402,7 +402,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
 // ------------------------------------------------------------- the computing warps
 // Rows past a sequence's own are zeros, their lse -inf, and there is nothing to
 // join for them; sequences are shared out over the blocks.
-template <int D, int kThreads>
+template <int D, int kThreads, int kRows>
 __device__ void att_pad_rows(const AttendArgs& A) {
   for (int b = blockIdx.x; b < A.S.B; b += gridDim.x) {
     int len, nv;
@@ -415,7 +415,7 @@ __device__ void att_pad_rows(const AttendArgs& A) {
                                 i % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
       if (i % (D / 8) == 0) A.lse[((int64_t)b * A.C.H + h) * A.S.n + t] = -INFINITY;
     }
-    const int full = (nv + kAttRows - 1) / kAttRows, none = A.groups - full;
+    const int full = (nv + kRows - 1) / kRows, none = A.groups - full;
     for (int64_t i = threadIdx.x; i < (int64_t)none * A.C.H; i += kThreads)
       A.rec[((int64_t)b * A.C.H + i / none) * A.groups + full + i % none] = make_int4(0, 0, 0, 0);
   }
@@ -425,7 +425,8 @@ __device__ __forceinline__ float att_lse(float m, float l) {
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, bool I8>
+// RG: rows of a segment, in eights.
+template <int D, bool I8, int RG>
 __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(AttendArgs A) {
   using Cfg = AttCfg<D, I8>;
   using T = std::conditional_t<I8, __half, bf16>;
@@ -448,19 +449,20 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   }
   __syncthreads();
   if (warp >= Cfg::kWarps) {
-    att_copy_warp<D, I8>(A, stages, full, empty, warp - Cfg::kWarps);
+    att_copy_warp<D, I8, RG>(A, stages, full, empty, warp - Cfg::kWarps);
     return;
   }
-  att_pad_rows<D, Cfg::kWarps * 32>(A);
+  att_pad_rows<D, Cfg::kWarps * 32, 8 * RG>(A);
 
   // weights are held 2^kUp times larger (f16 keeps those down to 2^-32 of the
   // reference), and a row's reference is moved only when a logit passes it by kOver
   constexpr float kUp = I8 ? 8.f : 0.f, kDown = I8 ? 0x1p-8f : 1.f, kOver = 7.f;
   const float cs = kLog2e / sqrtf((float)D);
-  uint32_t qa[2 * kSteps];  // Q as A operand: step s, a0 and a2 (rows g)
-  float o[kN][4];
-  float m = -INFINITY, l = 0.f;      // the row's reference; sum of this lane's weights
-  float qscale = 1.f, qbias = 0.f;   // int8: x is qa * qscale / 2^10; -128 sum qa / 2^24
+  // this lane's rows: g and, of sixteen, g + 8
+  uint32_t qa[RG][2 * kSteps];  // Q as A operand: step s, a0 and a2 (a1 and a3)
+  float o[kN][4];               // eight rows: low parts' sums in the second half
+  float m[RG], l[RG];           // a row's reference; sum of this lane's weights
+  float qscale[RG], qbias[RG];  // int8: x is qa * qscale / 2^10; -128 sum qa / 2^24
   float vref = -INFINITY;            // int8: o counts in units of the scale 2^vref
   int st = 0;
   uint32_t ph = 0;
@@ -483,54 +485,61 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
     const int flags = *reinterpret_cast<const volatile int*>(&mt->flags);
     if (flags & kEnd) break;
     if (flags & kFirst) {
-      const bool in = g < mt->rows;  // rows that are not there: zeros
-      const bf16* qp = A.x + mt->b * A.xs[0] + mt->h * A.xs[1] + (int64_t)(mt->q0 + (in ? g : 0)) * A.xs[2];
-      uint4 raw[D / 32];
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        // int8: dimensions 64 j + 16 t .. + 15 are steps 4 j .. 4 j + 3; bf16:
-        // dimensions 32 j + 8 t .. + 7 are steps 2 j and 2 j + 1
-        raw[j] = *reinterpret_cast<const uint4*>(
-            qp + (I8 ? 64 * (j >> 1) + 16 * t + 8 * (j & 1) : 32 * j + 8 * t));
+      for (int r = 0; r < RG; ++r) {
+        const int row = g + 8 * r;
+        const bool in = row < mt->rows;  // rows that are not there: zeros
+        const bf16* qp =
+            A.x + mt->b * A.xs[0] + mt->h * A.xs[1] + (int64_t)(mt->q0 + (in ? row : 0)) * A.xs[2];
+        uint4 raw[D / 32];
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j)
-        if (!in) raw[j] = make_uint4(0, 0, 0, 0);
-      if constexpr (I8) {
-        float f[D / 4], top = 0.f, sum = 0.f;
+        for (int j = 0; j < D / 32; ++j)
+          // int8: dimensions 64 j + 16 t .. + 15 are steps 4 j .. 4 j + 3; bf16:
+          // dimensions 32 j + 8 t .. + 7 are steps 2 j and 2 j + 1
+          raw[j] = *reinterpret_cast<const uint4*>(
+              qp + (I8 ? 64 * (j >> 1) + 16 * t + 8 * (j & 1) : 32 * j + 8 * t));
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) Vec16<bf16>::unpack(raw[j], f + 8 * j);
+        for (int j = 0; j < D / 32; ++j)
+          if (!in) raw[j] = make_uint4(0, 0, 0, 0);
+        if constexpr (I8) {
+          float f[D / 4], top = 0.f, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(f[i]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        // a power of two that brings the row's largest value to [2^14, 2^15)
-        const int e = max(-112, min(126, (int)(__float_as_uint(top) >> 23) - 127));
-        qscale = __uint_as_float((uint32_t)(e + 127) << 23);
-        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+          for (int j = 0; j < D / 32; ++j) Vec16<bf16>::unpack(raw[j], f + 8 * j);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          qa[i] = pack_h2(f[2 * i] * up, f[2 * i + 1] * up);
-          const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&qa[i]));
-          sum += r.x + r.y;
+          for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(f[i]));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+          // a power of two that brings the row's largest value to [2^14, 2^15)
+          const int e = max(-112, min(126, (int)(__float_as_uint(top) >> 23) - 127));
+          qscale[r] = __uint_as_float((uint32_t)(e + 127) << 23);
+          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            qa[r][i] = pack_h2(f[2 * i] * up, f[2 * i + 1] * up);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&qa[r][i]));
+            sum += h.x + h.y;
+          }
+          sum += __shfl_xor_sync(~0u, sum, 1);
+          sum += __shfl_xor_sync(~0u, sum, 2);
+          qbias[r] = -sum * 0x1p-17f;
+        } else {
+          qscale[r] = 1.f;
+          qbias[r] = 0.f;
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {
+            qa[r][4 * j] = raw[j].x;
+            qa[r][4 * j + 1] = raw[j].y;
+            qa[r][4 * j + 2] = raw[j].z;
+            qa[r][4 * j + 3] = raw[j].w;
+          }
         }
-        sum += __shfl_xor_sync(~0u, sum, 1);
-        sum += __shfl_xor_sync(~0u, sum, 2);
-        qbias = -sum * 0x1p-17f;
-      } else {
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          qa[4 * j] = raw[j].x;
-          qa[4 * j + 1] = raw[j].y;
-          qa[4 * j + 2] = raw[j].z;
-          qa[4 * j + 3] = raw[j].w;
-        }
+        m[r] = -INFINITY;
+        l[r] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-      m = -INFINITY;
-      l = 0.f;
       vref = -INFINITY;
     }
     if (__any_sync(~0u, !sm100::mbar_wait(&full[slot], ph))) {
@@ -540,13 +549,14 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
 
     // S, two tiles of eight tokens for each group of 16: column c of tile e is the
     // group's token 4 (c / 2) + 2 e + c % 2, so that this lane holds its tokens
-    // 4 t .. 4 t + 3 for row g
-    float p[NG][4];
+    // 4 t .. 4 t + 3 for its rows
+    float p[RG][NG][4];
+    auto q_of = [&](int r, int i) { return r < RG ? qa[r % RG][i] : 0u; };
 #pragma unroll
     for (int j = 0; j < NG; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float s[4] = {qbias, qbias, 0.f, 0.f};
+        float s[4] = {qbias[0], qbias[0], RG == 2 ? qbias[RG - 1] : 0.f, RG == 2 ? qbias[RG - 1] : 0.f};
         const unsigned char* kp = sp + (16 * j + 4 * (g >> 1) + 2 * e + (g & 1)) * D * Cfg::E + 16 * t;
 #pragma unroll
         for (int i = 0; i < D * Cfg::E / 64; ++i) {
@@ -558,95 +568,124 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
               uint32_t b0, b1;
               i8_to_sub(w[k], &b0, &b1);
               const int a = 2 * (4 * i + k);
-              mma_16816(s, qa[a], 0u, qa[a + 1], 0u, b0, b1, T());
+              mma_16816(s, q_of(0, a), q_of(1, a), q_of(0, a + 1), q_of(1, a + 1), b0, b1, T());
             }
           } else {
-            mma_16816(s, qa[4 * i], 0u, qa[4 * i + 1], 0u, u.x, u.y, T());
-            mma_16816(s, qa[4 * i + 2], 0u, qa[4 * i + 3], 0u, u.z, u.w, T());
+            mma_16816(s, q_of(0, 4 * i), q_of(1, 4 * i), q_of(0, 4 * i + 1), q_of(1, 4 * i + 1), u.x,
+                      u.y, T());
+            mma_16816(s, q_of(0, 4 * i + 2), q_of(1, 4 * i + 2), q_of(0, 4 * i + 3),
+                      q_of(1, 4 * i + 3), u.z, u.w, T());
           }
         }
-        p[j][2 * e] = s[0];
-        p[j][2 * e + 1] = s[1];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) {
+          p[r][j][2 * e] = s[2 * r];
+          p[r][j][2 * e + 1] = s[2 * r + 1];
+        }
       }
     const uint32_t ok = mt->ok;
     const int row0 = mt->len + mt->q0;  // position of row 0
-    float top = -INFINITY, vtop = -INFINITY;
+    float vtop = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const float4 kn = *reinterpret_cast<const float4*>(sp + Cfg::kNorm + (16 * j + 4 * t) * 4);
-      float f = cs;
-      if constexpr (I8) {
-        f *= mt->ks[j] * 1024.f * qscale;
-        vtop = fmaxf(vtop, mt->lv[j]);
+      if constexpr (I8) vtop = fmaxf(vtop, mt->lv[j]);
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        float f = cs;
+        if constexpr (I8) f *= mt->ks[j] * 1024.f * qscale[r];
+        p[r][j][0] *= kn.x * f;
+        p[r][j][1] *= kn.y * f;
+        p[r][j][2] *= kn.z * f;
+        p[r][j][3] *= kn.w * f;
       }
-      p[j][0] *= kn.x * f;
-      p[j][1] *= kn.y * f;
-      p[j][2] *= kn.z * f;
-      p[j][3] *= kn.w * f;
     }
     // units with tokens that some row must not see, or that are not there
     const bool tail = mt->t0 + Cfg::kTok > row0 || ok != (1u << NG) - 1;
     if (tail) {
 #pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        const int self = row0 + g - (mt->t0 + 16 * j + 4 * t);  // row g's own token
-        const bool there = ok >> j & 1;
+      for (int j = 0; j < NG; ++j)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          p[j][k] = k > self || !there ? -INFINITY : k == self ? kSelfLogit * kLog2e : p[j][k];
-      }
+        for (int r = 0; r < RG; ++r) {
+          const int self = row0 + g + 8 * r - (mt->t0 + 16 * j + 4 * t);  // the row's own token
+          const bool there = ok >> j & 1;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            p[r][j][k] = k > self || !there ? -INFINITY : k == self ? kSelfLogit * kLog2e : p[r][j][k];
+        }
     }
+    float top[RG];
+    bool over = I8 && vtop > vref;
 #pragma unroll
-    for (int j = 0; j < NG; ++j)
-      top = fmaxf(top, fmaxf(fmaxf(p[j][0], p[j][1]), fmaxf(p[j][2], p[j][3])));
-    if (__any_sync(~0u, top > m + kOver || vtop > vref)) {
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      float corr = 1.f;
-      if (top > m) {
-        corr = ex2(m - top);
-        m = top;
-        l *= corr;
+    for (int r = 0; r < RG; ++r) {
+      top[r] = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < NG; ++j)
+        top[r] = fmaxf(top[r], fmaxf(fmaxf(p[r][j][0], p[r][j][1]), fmaxf(p[r][j][2], p[r][j][3])));
+      over |= top[r] > m[r] + kOver;
+    }
+    if (__any_sync(~0u, over)) {
+      float corr[RG];
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
+        top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 2));
+        corr[r] = 1.f;
+        if (top[r] > m[r]) {
+          corr[r] = ex2(m[r] - top[r]);
+          m[r] = top[r];
+          l[r] *= corr[r];
+        }
+        if (I8 && vtop > vref) corr[r] *= ex2(vref - vtop);
       }
-      if (I8 && vtop > vref) {
-        corr *= ex2(vref - vtop);
-        vref = vtop;
-      }
+      if (I8) vref = fmaxf(vref, vtop);
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][k] *= corr;
+        for (int k = 0; k < 4; ++k) o[i][k] *= corr[RG == 2 ? k >> 1 : 0];
     }
     // P as A operand: the step of group j is its two tiles; bf16: high and low part
-    uint32_t a[NG][2], al[NG][2];
-    const float ref0 = m == -INFINITY ? 0.f : m - kUp;
+    uint32_t a[RG][NG][2], al[RG][NG][2];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      float ref = ref0, back = 1.f;
+      float lr = 0.f, back = 1.f;
       if constexpr (I8) {
         // weights carry the ratio of their group's scale to 2^vref (2^-64 is nothing
         // beside a step of it, and leaves its reciprocal in range)
-        const float lr = ok >> j & 1 ? fmaxf(mt->lv[j] - vref, -64.f) : 0.f;
-        ref -= lr;
+        lr = ok >> j & 1 ? fmaxf(mt->lv[j] - vref, -64.f) : 0.f;
         back = ex2(-lr);
       }
-      float sum = 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        p[j][k] = ex2(p[j][k] - ref);
-        sum += p[j][k];
-      }
-      l = I8 ? fmaf(sum, back, l) : l + sum;
+      for (int r = 0; r < RG; ++r) {
+        const float ref = (m[r] == -INFINITY ? 0.f : m[r] - kUp) - lr;
+        float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (I8) {
-          a[j][e] = pack_h2(p[j][2 * e], p[j][2 * e + 1]);
-          al[j][e] = 0u;
-        } else {
-          split2(p[j][2 * e], p[j][2 * e + 1], &a[j][e], &al[j][e]);
+        for (int k = 0; k < 4; ++k) {
+          p[r][j][k] = ex2(p[r][j][k] - ref);
+          sum += p[r][j][k];
+        }
+        l[r] = I8 ? fmaf(sum, back, l[r]) : l[r] + sum;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (I8) {
+            a[r][j][e] = pack_h2(p[r][j][2 * e], p[r][j][2 * e + 1]);
+            al[r][j][e] = 0u;
+          } else {
+            split2(p[r][j][2 * e], p[r][j][2 * e + 1], &a[r][j][e], &al[r][j][e]);
+          }
         }
       }
     }
+    // d += P V of group j's tokens for one tile of dimensions
+    auto product = [&](float (&d)[4], int j, uint32_t b0, uint32_t b1) {
+      if constexpr (RG == 1) {
+        mma_16816(d, a[0][j][0], al[0][j][0], a[0][j][1], al[0][j][1], b0, b1, T());
+      } else {
+        mma_16816(d, a[0][j][0], a[RG - 1][j][0], a[0][j][1], a[RG - 1][j][1], b0, b1, T());
+        if constexpr (!I8)
+          mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1], b0, b1, T());
+      }
+    };
     // v: four tokens of a dimension, 4 or 8 bytes
     const unsigned char* vp = sp + Cfg::kV + (g * 16 + 4 * t) * Cfg::E;
     auto load_v = [&](int j, int i, uint32_t* b0, uint32_t* b1) {
@@ -666,7 +705,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
         for (int j = 0; j < NG; ++j) {
           uint32_t b0, b1;
           load_v(j, i, &b0, &b1);
-          mma_16816(o[i], a[j][0], al[j][0], a[j][1], al[j][1], b0, b1, T());
+          product(o[i], j, b0, b1);
         }
     } else if constexpr (!I8) {
       // bf16 values that some row must not see: slots behind the last row, and
@@ -692,7 +731,9 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       }
       const bool apart = __any_sync(~0u, odd);
       for (int tk = 0; tk < (apart ? Cfg::kTok : 1); ++tk) {
-        const bool sees = !apart || mt->t0 + tk <= row0 + g;
+        bool sees[RG];
+#pragma unroll
+        for (int r = 0; r < RG; ++r) sees[r] = !apart || mt->t0 + tk <= row0 + g + 8 * r;
         const uint32_t half = tk & 1 ? 0xffff0000u : 0xffffu;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
@@ -704,39 +745,42 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
             const bool here = tk / 16 == j && tk % 16 / 4 == t;
             b0 &= !apart ? k0[j] : here && !(tk & 2) ? half & k0[j] : 0u;
             b1 &= !apart ? k1[j] : here && (tk & 2) ? half & k1[j] : 0u;
-            mma_16816(d, a[j][0], al[j][0], a[j][1], al[j][1], b0, b1, T());
+            product(d, j, b0, b1);
           }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (sees) o[i][k] += d[k];
+            if (sees[RG == 2 ? k >> 1 : 0]) o[i][k] += d[k];
         }
       }
     }
 
     if (flags & kLast) {
-      float L = l + __shfl_xor_sync(~0u, l, 1);
-      L += __shfl_xor_sync(~0u, L, 2);
-      L *= kDown;
-      if (g < mt->rows) {
-        float f1 = I8 && vref > -INFINITY ? exp2f(vref) * kDown : 1.f;
+#pragma unroll
+      for (int r = 0; r < RG; ++r) {
+        float L = l[r] + __shfl_xor_sync(~0u, l[r], 1);
+        L += __shfl_xor_sync(~0u, L, 2);
+        L *= kDown;
+        const int row = g + 8 * r;
+        if (row >= mt->rows) continue;
+        float f = I8 && vref > -INFINITY ? exp2f(vref) * kDown : 1.f;
+        auto value = [&](int i, int k) { return RG == 2 ? o[i][2 * r + k] : o[i][k] + o[i][2 + k]; };
         if (flags & kWhole) {
-          f1 *= L == 0.f ? 0.f : 1.f / L;
-          bf16* op = A.out + mt->b * A.os[0] + mt->h * A.os[1] + (int64_t)(mt->q0 + g) * A.os[2] + 2 * t;
+          f *= L == 0.f ? 0.f : 1.f / L;
+          bf16* op = A.out + mt->b * A.os[0] + mt->h * A.os[1] + (int64_t)(mt->q0 + row) * A.os[2] + 2 * t;
 #pragma unroll
           for (int i = 0; i < kN; ++i)
-            *reinterpret_cast<__nv_bfloat162*>(op + 8 * i) = __floats2bfloat162_rn(
-                (o[i][0] + o[i][2]) * f1, (o[i][1] + o[i][3]) * f1);
+            *reinterpret_cast<__nv_bfloat162*>(op + 8 * i) =
+                __floats2bfloat162_rn(value(i, 0) * f, value(i, 1) * f);
           if (t == 0)
-            A.lse[((int64_t)mt->b * A.C.H + mt->h) * A.S.n + mt->q0 + g] = att_lse(m, L);
+            A.lse[((int64_t)mt->b * A.C.H + mt->h) * A.S.n + mt->q0 + row] = att_lse(m[r], L);
         } else {
           const int64_t run = (int64_t)warp * gridDim.x + blockIdx.x;
-          const int64_t row = (run * 2 + mt->slot) * 8 + g;
+          const int64_t at = (run * 2 + mt->slot) * 8 * RG + row;
 #pragma unroll
           for (int i = 0; i < kN; ++i)
-            *reinterpret_cast<float2*>(A.part + row * D + 8 * i + 2 * t) =
-                make_float2((o[i][0] + o[i][2]) * f1, (o[i][1] + o[i][3]) * f1);
-          if (t == 0)
-            *reinterpret_cast<float2*>(A.part_ml + row * 2) = make_float2(m, L);
+            *reinterpret_cast<float2*>(A.part + at * D + 8 * i + 2 * t) =
+                make_float2(value(i, 0) * f, value(i, 1) * f);
+          if (t == 0) *reinterpret_cast<float2*>(A.part_ml + at * 2) = make_float2(m[r], L);
         }
       }
     }
@@ -755,8 +799,8 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
 // block, eight lanes for a part, so that all parts' loads are under way at once:
 // the time is that of two loads from L2 in turn and the launch. The order in
 // which parts are summed is that of their numbers.
-// grid (segments, up to 8 rows, D / 32), block 8 x parts or so, 32 .. 256.
-template <int D>
+// grid (segments, up to kRows rows, D / 32), block 8 x parts or so, 32 .. 256.
+template <int D, int kRows>
 __global__ void __launch_bounds__(256) k_cache_combine(AttendArgs A) {
   constexpr int kAt = 5;  // parts of a lane that are fetched together
   const int lane8 = threadIdx.x & 7, ps = threadIdx.x >> 3, slots = blockDim.x >> 3;
@@ -780,7 +824,7 @@ __global__ void __launch_bounds__(256) k_cache_combine(AttendArgs A) {
       ml[i] = make_float2(-INFINITY, 0.f);
       pv[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (j < count) {
-        const int64_t at = (((int64_t)r.x + j) * 2 + (j == 0)) * kAttRows + row;
+        const int64_t at = (((int64_t)r.x + j) * 2 + (j == 0)) * kRows + row;
         ml[i] = *reinterpret_cast<const float2*>(A.part_ml + at * 2);
         pv[i] = *reinterpret_cast<const float4*>(A.part + at * D + dim0 + lane8 * 4);
       }
@@ -836,7 +880,7 @@ __global__ void __launch_bounds__(256) k_cache_combine(AttendArgs A) {
     L += sl[w] * f;
     sum += so[w][lane] * f;
   }
-  const int grp = seg % A.groups, bh = seg / A.groups, t = grp * kAttRows + row;
+  const int grp = seg % A.groups, bh = seg / A.groups, t = grp * kRows + row;
   const int b = bh / A.C.H, h = bh - b * A.C.H;
   A.out[b * A.os[0] + h * A.os[1] + (int64_t)t * A.os[2] + dim0 + lane] =
       __float2bfloat16_rn(L == 0.f ? 0.f : sum / L);

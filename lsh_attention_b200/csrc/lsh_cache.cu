@@ -186,9 +186,9 @@ lsh_status launch_append(const AppendArgs& A, bool i8, cudaStream_t st) {
 }
 
 // Workspace of the cached attention: for every segment a record, and for every
-// computing warp two partial results of eight rows.
+// computing warp two partial results of a segment's rows.
 struct AttendLayout {
-  int blocks, groups;
+  int blocks, rows, groups;  // rows of a segment; segments of a (sequence, head)
   int64_t segments;
   size_t ml, part, total;
 };
@@ -196,10 +196,13 @@ struct AttendLayout {
 AttendLayout attend_layout(const lsh_cache_desc& c, const lsh_cache_rows& r) {
   AttendLayout L;
   L.blocks = sm_count();
-  L.groups = (r.n + kAttRows - 1) / kAttRows;
+  // calls of more than eight rows take sixteen together: the cache is read once for
+  // them, and a product's other eight rows cost nothing
+  L.rows = r.n > 8 ? 16 : 8;
+  L.groups = (r.n + L.rows - 1) / L.rows;
   L.segments = (int64_t)r.batch * c.heads * L.groups;
   const int warps = c.d == 64 ? AttCfg<64, false>::kWarps : AttCfg<128, false>::kWarps;
-  const size_t rows = (size_t)L.blocks * warps * 2 * kAttRows;
+  const size_t rows = (size_t)L.blocks * warps * 2 * L.rows;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   L.ml = up((size_t)L.segments * sizeof(int4));
   L.part = L.ml + up(rows * 2 * sizeof(float));
@@ -207,13 +210,13 @@ AttendLayout attend_layout(const lsh_cache_desc& c, const lsh_cache_rows& r) {
   return L;
 }
 
-template <int D, bool I8>
-lsh_status launch_attend(const AttendArgs& A, const AttendLayout& L, cudaStream_t st) {
+template <int D, bool I8, int RG>
+lsh_status launch_attend_rows(const AttendArgs& A, const AttendLayout& L, cudaStream_t st) {
   using Cfg = AttCfg<D, I8>;
   static_assert(Cfg::kWarps * Cfg::kDepth <= 32, "barriers");
   static_assert(sizeof(UnitMeta) <= 128 && Cfg::kStage % 16 == 0, "stage header");
   static_assert(Cfg::kSmem <= 227 * 1024, "shared memory");
-  auto kern = k_cache_attend<D, I8>;
+  auto kern = k_cache_attend<D, I8, RG>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, Cfg::kSmem, &done)) return LSH_ERR_CUDA;
   kern<<<L.blocks, Cfg::kThreads, Cfg::kSmem, st>>>(A);
@@ -224,14 +227,19 @@ lsh_status launch_attend(const AttendArgs& A, const AttendLayout& L, cudaStream_
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)L.segments, (unsigned)std::min(A.S.n, kAttRows), D / 32);
+  cfg.gridDim = dim3((unsigned)L.segments, (unsigned)std::min(A.S.n, 8 * RG), D / 32);
   // a segment has about this many parts where it is shared at all
   const int64_t parts = (int64_t)L.blocks * Cfg::kWarps / L.segments + 2;
   cfg.blockDim = dim3(32u * (unsigned)std::min<int64_t>(8, (parts + 3) / 4));
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_cache_combine<D>, A) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_cache_combine<D, 8 * RG>, A) == cudaSuccess ? LSH_OK : LSH_ERR_CUDA;
+}
+
+template <int D, bool I8>
+lsh_status launch_attend(const AttendArgs& A, const AttendLayout& L, cudaStream_t st) {
+  return L.rows == 8 ? launch_attend_rows<D, I8, 1>(A, L, st) : launch_attend_rows<D, I8, 2>(A, L, st);
 }
 
 }  // namespace

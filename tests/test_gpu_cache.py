@@ -373,7 +373,7 @@ def check_attend(gpu, ref, table, q, lens, valid=None, **kw):
     ([0], 1, None),                          # alone: its own value, lse -1e5
     ([1, 15, 16], 1, None), ([127, 128, 300], 1, None),
     ([0, 5, 63], 3, None), ([200, 0, 31], 8, [8, 0, 5]), ([10, 129, 64], 9, [9, 1, 8]),
-    ([33, 100], 17, None),
+    ([33, 100], 17, None), ([5, 120], 11, [11, 4]), ([0, 77], 33, [20, 33]), ([128, 250], 16, None),
 ])
 def test_attend(d, page, int8, lens, n, valid):
     ref, table, q = filled(len(lens), 2, d, page, int8, lens, n)
@@ -460,10 +460,11 @@ def test_attend_sharp_and_flat_rows():
         near(lse, rl, 60 * 2.0 ** -13 + rl.abs() * 2.0 ** -23, "lse")
 
 
-def test_attend_does_not_see_what_is_masked():
+@pytest.mark.parametrize("n", [5, 12])
+def test_attend_does_not_see_what_is_masked(n):
     """Slots past the sequence hold NaN, a later token's value and key infinities: a row sees
     neither; a NaN query spoils its own row only."""
-    lens, n = [45], 5
+    lens = [45]
     ref, table, q = filled(1, 2, 64, 16, False, lens, n)
     page, slot = int(table[0, 48 // 16]), 48 % 16
     ref["v"][page, :, 0, :, slot] = math.inf
@@ -477,7 +478,7 @@ def test_attend_does_not_see_what_is_masked():
         near(out[0, h, t], ro[0, h, t], ro[0, h, t].abs() * 2.0 ** -8 + mag[0, h, t] * 2.0 ** -13, "out")
         near(lse[0, h, t], rl[0, h, t], 2.0 ** -12, "lse")
     assert torch.isnan(out[0, 1, 1]).all()
-    assert not torch.isfinite(out[0, :, 4]).any()  # sees the infinite key and value
+    assert not torch.isfinite(out[0, :, 4:]).any()  # see the infinite key and value
 
 
 def test_bad_tables_are_reported_and_skipped():
