@@ -34,7 +34,18 @@
 // the product starts from. One of V becomes the f16 number 1152 + q, less 1152. Both
 // are exact. Rows of x are f16 scaled by a power of two to a largest value in
 // [2^14, 2^15): exact but for values below 2^-31 of it. Weights are rounded to
-// f16 once (2^-11), at 2^8 times their size.
+// f16 once (2^-11), at 2^8 times their size: as bf16 results are to 2^-8.
+//
+// Measured (main kernel / with the joining of parts and both launches), of the copy
+// rate: one token over 65536, 8 heads of 128, bf16: 48.8 us (0.85) / 53; 64 sequences
+// of up to 12288, 8 heads of 64, int8: 78 us (0.81) / 83; five rows of 16 sequences,
+// bf16 d 128: 41 / 45. What is left: 3.5 us before the first copy (lengths, the
+// place of the run, pages, scales: one load after the other), the joining, and in int8
+// 12 us of instructions that DRAM does not hide. Built and slower: eight warps on
+// the same 128 tokens with a barrier for each segment (129 us for the int8 case:
+// short segments wait); one ring for all warps (its stages change hands, 134);
+// one copying warp (194); parts joined by the last of eight neighbours, counted
+// with atomics, instead of a second kernel (99: the fences wait for loads under way).
 #pragma once
 
 #include <cuda_fp16.h>
