@@ -174,9 +174,9 @@ __device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
 // One block: R consecutive token slots of one sequence for a few heads. The sines
 // of its tokens are formed once and serve its heads; the next two heads' rows
 // travel (cp.async) meanwhile. A thread takes 16-byte pieces of rows of x: 1/||x||,
-// the rotation with the partners from shared memory, the rotated piece out. v leaves through transposed 8x8 tiles (ldmatrix), so that a
-// thread stores four tokens of a dimension together and a warp whole sectors of
-// the groups. int8: pieces wait in registers for the page's largest magnitude
+// the rotation with the partners from shared memory, the rotated piece out. v
+// leaves through transposed 8x8 tiles (ldmatrix), so that a thread stores four
+// tokens of a dimension together and a warp whole sectors of the groups. int8: pieces wait in registers for the page's largest magnitude
 // (maxima of non-negative floats by integer atomicMax in shared memory: the same
 // whatever the order); this block alone owns the page's head, so earlier rows
 // are rounded again in place. A stream of rows in and out, bound by DRAM in bf16: 64
@@ -218,9 +218,10 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
   // the block's slots: positions base .. base + R - 1; new rows [r0, r1) of them
   const int span = I8 && C.P > R ? C.P : R;  // tokens between blocks
   int64_t base = (int64_t)(len / span + blockIdx.x) * span;
+  const int64_t end = min(base + span, (int64_t)len + nv);
   if (span > R) base += max((int64_t)0, len - base) & ~(kGroup - 1);
   const int r0 = (int)max((int64_t)0, len - base);
-  const int r1 = (int)max((int64_t)0, min((int64_t)R, (int64_t)len + nv - base));
+  const int r1 = (int)max((int64_t)0, min((int64_t)R, end - base));
   if (r0 >= r1) return;
   const int tok0 = (int)(base - len);  // row r is the call's row tok0 + r
 

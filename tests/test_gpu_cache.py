@@ -233,6 +233,30 @@ def test_append(d, page, int8, pieces):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("n", [2, 5, 16, 17, 18])
+def test_append_few_rows_across_a_page_end(n, d, page, int8):
+    """A handful of rows that begin in one page and end in the next, at every place of it. Bit for
+    bit, in the slots behind them too."""
+    H = 2
+    lens = sorted({page - 1, page - 2, page - n + 1, page - n, page - n - 1, page - 16, 2 * page - 3} -
+                  {p for p in range(-32, 0)})
+    B = len(lens)
+    table = table_of(B, 3, 3 * B + 1)
+    ref = oc.empty(3 * B + 1, H, page, d, int8)
+    gpu = to_gpu(ref)
+    for i, (at, m) in enumerate([([0] * B, max(lens)), (lens, n)]):
+        x, v = (randn(B, H, m, d, seed=2 * i + s).bfloat16() * 2.0 ** i for s in (0, 1))
+        valid = lens if i == 0 else None
+        oc.append(ref, x, v, table, at, valid)
+        seq = torch.tensor(at, dtype=torch.int32).cuda()
+        nv = None if valid is None else torch.tensor(valid, dtype=torch.int32).cuda()
+        lb.lsh_cache_append(gpu, x.cuda(), v.cuda(), table.cuda(), seq, n_valid=nv)
+        same_cache(gpu, ref)
+    assert gpu.get_device_status() == 0
+
+
+@pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("d,dims,adjacent", [(64, (24, 24, 16), False), (64, (40,), True),
                                              (128, (128,), True), (128, (128,), False),
                                              (128, (44, 42, 42), False), (64, (16, 12, 12, 8), False)])
