@@ -352,8 +352,8 @@ typedef struct {
 /* Rotary positions: pair (lo, hi) of axis a, the p-th pair of all, turns by
  * t = positions[a] * freqs[p]:
  *   out[lo] = x[lo] cos t - x[hi] sin t,  out[hi] = x[lo] sin t + x[hi] cos t.
- * The angle is formed in fp64 and reduced there, so far positions keep their
- * precision; the rotation is fp32 and rounds once. inverse = 1 is the
+ * The angle is formed as a fraction of a turn in 64 bits, so far positions keep
+ * their precision; the rotation is fp32 and rounds once. inverse = 1 is the
  * gradient with respect to x (and undoes the call). positions int32, any sign;
  * freqs [sum dims / 2] fp32. out may be x itself with the same strides, else
  * they must not overlap. */

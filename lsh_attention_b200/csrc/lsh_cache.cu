@@ -82,8 +82,8 @@ template <typename T, int D>
 lsh_status launch_rope(RopeArgs A, const void* x, void* out, cudaStream_t st) {
   constexpr int N = 16 / sizeof(T), kTok = 256 / (D / N);
   A.tiles = (A.n + kTok - 1) / kTok;
-  // four blocks an SM are resident; heads are split over jobs where there are
-  // fewer tiles
+  // four blocks an SM or more are resident; heads are split over jobs where there
+  // are fewer tiles
   const int64_t want = 4 * sm_count(), tiles = (int64_t)A.tiles * A.B;
   const int groups = (int)std::min<int64_t>(A.H, std::max<int64_t>(1, want / tiles));
   A.heads_per = (A.H + groups - 1) / groups;
@@ -99,7 +99,7 @@ lsh_status launch_rope(RopeArgs A, const void* x, void* out, cudaStream_t st) {
   }
   // Neighbouring pairs: a job a block (0.91 of the copy rate at B1 H8 n65536 d128;
   // persistent blocks 0.84). Halves have more to work out before the first row:
-  // persistent blocks (0.72 at B8 H8 n12288 d64, axes 24, 24, 16; a job a block 0.61).
+  // persistent blocks (0.75 at B8 H8 n12288 d64, axes 24, 24, 16; a job a block 0.61).
   const int64_t jobs = tiles * A.head_groups;
   const int64_t most = A.rot.adjacent ? INT32_MAX : 5 * sm_count();
   const int64_t blocks = std::min(jobs, most), rest = blocks / A.tiles;

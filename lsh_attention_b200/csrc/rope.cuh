@@ -179,8 +179,8 @@ struct RopeArgs {
 // piece lies, the phases, the angles. Rows come by cp.async, two batches of heads
 // ahead, and are under way meanwhile. Halves: the lanes of a row form each angle
 // once and find their partners' pieces in shared memory. Measured: 45 us at B1 H8
-// n65536 d128, neighbours (0.91 of the copy rate), 39 us at B8 H8 n12288 d64, axes
-// 24, 24, 16 by halves (0.79; with partners read from global memory too, 95 us; a
+// n65536 d128, neighbours (0.91 of the copy rate), 41 us at B8 H8 n12288 d64, axes
+// 24, 24, 16 by halves (0.75; with partners read from global memory too, 95 us; a
 // position fetched for each angle when it is formed, 43 us).
 // grid (blocks), block 256.
 template <typename T, int D, int W, bool ADJ>
