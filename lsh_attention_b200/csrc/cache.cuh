@@ -176,8 +176,8 @@ __device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
 // travel (cp.async) meanwhile. A thread takes 16-byte pieces of rows of x: 1/||x||,
 // the rotation with the partners from shared memory, the rotated piece out. v
 // leaves through transposed 8x8 tiles (ldmatrix), so that a thread stores four
-// tokens of a dimension together and a warp whole sectors of the groups. int8: pieces wait in registers for the page's largest magnitude
-// (maxima of non-negative floats by integer atomicMax in shared memory: the same
+// tokens of a dimension together and a warp whole sectors of the groups. int8:
+// pieces wait in registers for the page's largest magnitude (maxima of non-negative floats by integer atomicMax in shared memory: the same
 // whatever the order); this block alone owns the page's head, so earlier rows
 // are rounded again in place. A stream of rows in and out, bound by DRAM in bf16: 64
 // us for 4 x 8192 rows of 8 heads of 128 with a rotation (0.80 of the copy rate; 48 us

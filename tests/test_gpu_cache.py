@@ -298,6 +298,27 @@ def test_append_rotates(d, dims, adjacent, int8):
     assert torch.equal(y, xr) and torch.equal(bits(a.k), bits(c.k))
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n", [1, 6, 17, 40])
+@pytest.mark.parametrize("d,page", [(64, 128), (128, 64)])
+def test_append_rotates_across_a_page_end(d, page, n, int8):
+    """A few rows behind others, turned on the way or before: the same cache, bit for bit."""
+    B, H, dims = 3, 5, (24, 24, 16)
+    table = table_of(B, 3, 10).cuda()
+    x, v = randn(B, H, n, d).bfloat16().cuda(), randn(B, H, n, d, seed=1).bfloat16().cuda()
+    pos = torch.randint(0, 100000, (3, B, n), generator=torch.Generator().manual_seed(3)).int().cuda()
+    f = freqs_of(dims).cuda()
+    seq = torch.tensor([page - 1, page - 5, 2 * page - 16], dtype=torch.int32).cuda()
+    a, b = (to_gpu(oc.empty(10, H, page, d, int8, fill=0.5)) for _ in range(2))
+    xr = lb.lsh_cache_append(a, x, v, table, seq, positions=pos, freqs=f, axis_dims=dims)
+    rows = lb.lsh_rope(x, pos, f, axis_dims=dims)
+    lb.lsh_cache_append(b, rows, v, table, seq)
+    assert torch.equal(xr, rows)
+    assert torch.equal(bits(a.k), bits(b.k)) and torch.equal(bits(a.v), bits(b.v))
+    if int8:
+        assert torch.equal(a.k_scale, b.k_scale) and torch.equal(a.v_scale, b.v_scale)
+
+
 def test_append_extremes():
     """Short and long rows: the norm's squares neither vanish nor overflow; int8 scales reach both
     ends; infinities and NaN are held at the ends of the range and reported."""
@@ -450,6 +471,20 @@ def test_attend_work_of_every_shape(B, H, d, page, lens, n, int8):
     ref, table, q = random_cache(B, H, d, page, int8, lens, n)
     valid = None if n == 1 else [(n + b) % (n + 1) for b in range(B)]
     check_attend(to_gpu(ref), ref, table, q, lens, valid)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("B,n,lens,valid", [
+    (3, 4, [5, 0, 90], [0, 0, 0]),                                   # no row at all
+    (70, 2, [7 * i for i in range(70)], [0] * 40 + [2] + [0] * 28 + [1]),  # long runs of none
+    (1, 300, [50], [290]),                                           # many row groups
+    (2, 16, [0, 3], [16, 15]),
+])
+def test_attend_few_rows_of_many(B, n, lens, valid, int8):
+    ref, table, q = random_cache(B, 2, 64, 32, int8, lens, n, seed=9)
+    out, lse = check_attend(to_gpu(ref), ref, table, q, lens, valid)
+    for b in range(B):
+        assert (out[b, :, valid[b]:] == 0).all() and torch.isneginf(lse[b, :, valid[b]:]).all()
 
 
 @pytest.mark.parametrize("int8", [False, True])
