@@ -177,12 +177,14 @@ __device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
 // the rotation with the partners from shared memory, the rotated piece out. v
 // leaves through transposed 8x8 tiles (ldmatrix), so that a thread stores four
 // tokens of a dimension together and a warp whole sectors of the groups. int8:
-// pieces wait in registers for the page's largest magnitude (maxima of non-negative floats by integer atomicMax in shared memory: the same
-// whatever the order); this block alone owns the page's head, so earlier rows
-// are rounded again in place. A stream of rows in and out, bound by DRAM in bf16: 64
+// pieces wait in registers for the page's largest magnitude (maxima of
+// non-negative floats by integer atomicMax in shared memory: the same whatever the
+// order); this block alone owns the page's head, so earlier rows are rounded again
+// in place. A stream of rows in and out, bound by DRAM in bf16: 64
 // us for 4 x 8192 rows of 8 heads of 128 with a rotation (0.80 of the copy rate; 48 us
-// without one, which writes a third less). int8 waits for the page's maximum twice a
-// head and is bound by its barriers and instructions: 96 us there (0.43).
+// without one, which writes a third less). int8 is bound by its instructions (two
+// thirds of the issue slots, with DRAM mostly idle): 94 us there (0.43); with every
+// thread forming the scales itself, two barriers of a head's four left out, 96.
 // grid (blocks of rows, head groups, batch), block append_threads(D, R).
 template <int D, bool I8, int R, int TURN>
 __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D, R))

@@ -317,7 +317,8 @@ lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
   const int rows_per = append_rows(i8, A.C.P, A.S.n), span = i8 ? std::max(A.C.P, rows_per) : rows_per;
   const int64_t blocks = (int64_t)((A.S.n + span - 2) / span + 1) * A.S.B;
   // heads are split over blocks until these fill the card twice: every block forms
-  // its tokens' angles again
+  // its tokens' angles again (8 int8 sequences of up to 2000 rows, H8 d64: 25 us; once
+  // 35, three times 28)
   const int threads = append_threads(A.C.d, rows_per);
   const int64_t want = 2 * (1024 / threads) * sm_count();
   const int groups = (int)std::min<int64_t>(A.C.H, std::max<int64_t>(1, want / blocks));
