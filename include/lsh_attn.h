@@ -446,7 +446,9 @@ lsh_status lsh_cache_attend_workspace_size(const lsh_cache_desc *desc,
  *   x_t . k_j key_inv_norm_j / sqrt(d),   and -1e5 for itself (j = p),
  * as lsh_attn_dense_forward does with causal = 1; x are the (rotated) rows in
  * bf16, k_j and v_j the cache's values. Products x_t . k_j are fp32 sums of the
- * rows as they are: ||x_t|| ||x_j|| has to stay below 2^100.
+ * rows as they are: ||x_t|| ||x_j|| has to stay below 2^100. Weights times values are
+ * fp32 sums too, of weights to 2^-17 of each (of an int8 page whose v_scale lies 2^100
+ * below another's, values may count as zeros).
  *   out bf16 (out_stride), lse [batch][heads][n] fp32, natural log.
  * Rows past n_valid, and rows that see nothing (bad pages), are zeros with
  * lse = -inf. Made for few tokens a sequence (one, or a handful of drafted

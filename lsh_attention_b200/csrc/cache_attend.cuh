@@ -23,18 +23,19 @@
 // may be permuted at will as long as both operands agree, so a lane takes
 // dimensions of K (16 bytes) and tokens of V (four of a group of 16, which lies
 // dimension by dimension in the cache) that are consecutive in memory, and feeds
-// them to the products as they are: no transposes, no shuffles. bf16 weights go in
-// high and low parts, 2^-17 together, so that P V loses nothing against fp32
-// ones: of eight rows in one product, whose 16 rows hold both, of sixteen (calls
-// of more than eight rows) in two.
+// them to the products as they are: no transposes, no shuffles. Weights go in as
+// high and low parts in bf16, 2^-17 together whatever their size, so that P V loses
+// nothing against fp32 ones: of eight rows in one product, whose 16 rows hold both,
+// of sixteen (calls of more than eight rows) in two.
 //
 // int8: what bounds the kernel besides DRAM is the instructions that widen the
 // bytes. A byte of K becomes the f16 subnormal (q + 128) 2^-24 by being put under
 // a zero (one byte permutation for two); the 128 comes off as -128 sum x, which
-// the product starts from. One of V becomes the f16 number 1152 + q, less 1152. Both
-// are exact. Rows of x are f16 scaled by a power of two to a largest value in
-// [2^14, 2^15): exact but for values below 2^-31 of it. Weights are rounded to
-// f16 once (2^-11), at 2^8 times their size: as bf16 results are to 2^-8.
+// the product starts from. One of V becomes the bf16 number (q + 128) 2^-133, and by
+// one multiply-add q / 64. Both are exact. Rows of x are f16 scaled by a power of two
+// to a largest value in [2^14, 2^15): exact but for values below 2^-31 of it. A weight
+// is multiplied by its page's scale before it is split: bf16 has the range for it, so
+// that no page's scale costs another page's weights any bits.
 //
 // Measured (main kernel / with the joining of parts and both launches), of the copy
 // rate: one token over 65536, 8 heads of 128, bf16: 48.8 us (0.85) / 53; 64 sequences
@@ -78,7 +79,7 @@ struct UnitMeta {
   int flags, slot;      // kFirst ...; slot of a partial result
   int n;                // the unit's number in the warp's run
   uint32_t ok;          // bit s: tokens 16 s .. of the unit are there
-  float ks[4], lv[4];   // int8: scales of k, log2 of those of v
+  float ks[4], vs[4];   // int8: scales of k and v
 };
 // of the warp's units of a segment: the first, the last, all; nothing follows
 constexpr int kFirst = 1, kLast = 2, kWhole = 4, kEnd = 8;
@@ -117,16 +118,18 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four int8 to two pairs of f16: 1024 + (q + 128) is written into the mantissa
-// and 1152 taken off, both exact.
-__device__ __forceinline__ void i8_to_f16(uint32_t w, uint32_t* b0, uint32_t* b1) {
+// Four int8 to two pairs of bf16, q / 64: a byte under a zero is the bf16 number
+// (q + 128) 2^-133 (its eighth bit is the lowest exponent's); times 2^127, less 2.
+// All exact.
+__device__ __forceinline__ void i8_to_bf16(uint32_t w, uint32_t* b0, uint32_t* b1) {
   w ^= 0x80808080u;
-  const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-  uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
-  __half2 a = __hsub2(*reinterpret_cast<__half2*>(&lo), off);
-  __half2 b = __hsub2(*reinterpret_cast<__half2*>(&hi), off);
-  *b0 = *reinterpret_cast<uint32_t*>(&a);
-  *b1 = *reinterpret_cast<uint32_t*>(&b);
+  const __nv_bfloat162 up = __bfloat162bfloat162(__ushort_as_bfloat16(0x7f00));   // 2^127
+  const __nv_bfloat162 off = __bfloat162bfloat162(__ushort_as_bfloat16(0xc000));  // -2
+  uint32_t lo = __byte_perm(w, 0u, 0x4140), hi = __byte_perm(w, 0u, 0x4342);
+  const __nv_bfloat162 a = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&lo), up, off);
+  const __nv_bfloat162 b = __hfma2(*reinterpret_cast<__nv_bfloat162*>(&hi), up, off);
+  *b0 = *reinterpret_cast<const uint32_t*>(&a);
+  *b1 = *reinterpret_cast<const uint32_t*>(&b);
 }
 // Four int8 to two pairs of f16 subnormals, (q + 128) 2^-24.
 __device__ __forceinline__ void i8_to_sub(uint32_t w, uint32_t* b0, uint32_t* b1) {
@@ -352,7 +355,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
       const uint32_t ok = (__ballot_sync(mine, cur.id >= 0) >> (4 * q)) & 15;
       if (I8) {
         mt->ks[sl] = ks;
-        mt->lv[sl] = cur.id >= 0 ? log2f(vs) : -INFINITY;
+        mt->vs[sl] = vs;
       }
       if (sl == 0) {
         mt->b = cur.b;
@@ -465,16 +468,17 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   }
   att_pad_rows<D, Cfg::kWarps * 32, 8 * RG>(A);
 
-  // weights are held 2^kUp times larger (f16 keeps those down to 2^-32 of the
-  // reference), and a row's reference is moved only when a logit passes it by kOver
-  constexpr float kUp = I8 ? 8.f : 0.f, kDown = I8 ? 0x1p-8f : 1.f, kOver = 7.f;
+  constexpr float kOver = 7.f;  // a row's reference is moved when a logit passes it by that
   const float cs = kLog2e / sqrtf((float)D);
   // this lane's rows: g and, of sixteen, g + 8
   uint32_t qa[RG][2 * kSteps];  // Q as A operand: step s, a0 and a2 (a1 and a3)
   float o[kN][4];               // eight rows: low parts' sums in the second half
+                                // (int8: in units of 64 vref)
   float m[RG], l[RG];           // a row's reference; sum of this lane's weights
   float qscale[RG], qbias[RG];  // int8: x is qa * qscale / 2^10; -128 sum qa / 2^24
-  float vref = -INFINITY;            // int8: o counts in units of the scale 2^vref
+  // int8: a power of two, a scale of v that was met, and 1 / vref. It is moved only by
+  // a scale 2^64 times larger: its purpose is the range alone, any ratio is exact
+  float vref = 0.f, vinv = 0.f;
   int st = 0;
   uint32_t ph = 0;
 
@@ -551,7 +555,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-      vref = -INFINITY;
+      vref = vinv = 0.f;
     }
     if (__any_sync(~0u, !sm100::mbar_wait(&full[slot], ph))) {
       late = true;
@@ -596,11 +600,11 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       }
     const uint32_t ok = mt->ok;
     const int row0 = mt->len + mt->q0;  // position of row 0
-    float vtop = -INFINITY;
+    float vtop = 0.f;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const float4 kn = *reinterpret_cast<const float4*>(sp + Cfg::kNorm + (16 * j + 4 * t) * 4);
-      if constexpr (I8) vtop = fmaxf(vtop, mt->lv[j]);
+      if constexpr (I8) vtop = fmaxf(vtop, mt->vs[j]);
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
         float f = cs;
@@ -626,7 +630,8 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
         }
     }
     float top[RG];
-    bool over = I8 && vtop > vref;
+    const bool vover = I8 && vtop > vref * 0x1p64f;
+    bool over = vover;
 #pragma unroll
     for (int r = 0; r < RG; ++r) {
       top[r] = -INFINITY;
@@ -636,7 +641,13 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       over |= top[r] > m[r] + kOver;
     }
     if (__any_sync(~0u, over)) {
-      float corr[RG];
+      float corr[RG], down = 1.f;
+      if (vover) {
+        const float was = vref;
+        vref = __uint_as_float(min(max(__float_as_uint(vtop) & 0x7f800000u, 0x00800000u), 0x7e800000u));
+        vinv = recip2(vref);
+        down = was * vinv;
+      }
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
         top[r] = fmaxf(top[r], __shfl_xor_sync(~0u, top[r], 1));
@@ -647,54 +658,42 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
           m[r] = top[r];
           l[r] *= corr[r];
         }
-        if (I8 && vtop > vref) corr[r] *= ex2(vref - vtop);
+        if (I8) corr[r] *= down;
       }
-      if (I8) vref = fmaxf(vref, vtop);
 #pragma unroll
       for (int i = 0; i < kN; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[i][k] *= corr[RG == 2 ? k >> 1 : 0];
     }
-    // P as A operand: the step of group j is its two tiles; bf16: high and low part
+    // P as A operand: the step of group j is its two tiles; high and low part
     uint32_t a[RG][NG][2], al[RG][NG][2];
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      float lr = 0.f, back = 1.f;
-      if constexpr (I8) {
-        // weights carry the ratio of their group's scale to 2^vref (2^-64 is nothing
-        // beside a step of it, and leaves its reciprocal in range)
-        lr = ok >> j & 1 ? fmaxf(mt->lv[j] - vref, -64.f) : 0.f;
-        back = ex2(-lr);
-      }
+      // int8: weights of V carry their group's scale
+      const float vs = I8 ? mt->vs[j] * vinv : 1.f;
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
-        const float ref = (m[r] == -INFINITY ? 0.f : m[r] - kUp) - lr;
+        const float ref = m[r] == -INFINITY ? 0.f : m[r];
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           p[r][j][k] = ex2(p[r][j][k] - ref);
           sum += p[r][j][k];
+          if (I8) p[r][j][k] *= vs;
         }
-        l[r] = I8 ? fmaf(sum, back, l[r]) : l[r] + sum;
+        l[r] += sum;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if constexpr (I8) {
-            a[r][j][e] = pack_h2(p[r][j][2 * e], p[r][j][2 * e + 1]);
-            al[r][j][e] = 0u;
-          } else {
-            split2(p[r][j][2 * e], p[r][j][2 * e + 1], &a[r][j][e], &al[r][j][e]);
-          }
-        }
+        for (int e = 0; e < 2; ++e)
+          split2(p[r][j][2 * e], p[r][j][2 * e + 1], &a[r][j][e], &al[r][j][e]);
       }
     }
     // d += P V of group j's tokens for one tile of dimensions
     auto product = [&](float (&d)[4], int j, uint32_t b0, uint32_t b1) {
       if constexpr (RG == 1) {
-        mma_16816(d, a[0][j][0], al[0][j][0], a[0][j][1], al[0][j][1], b0, b1, T());
+        mma_16816(d, a[0][j][0], al[0][j][0], a[0][j][1], al[0][j][1], b0, b1, bf16());
       } else {
-        mma_16816(d, a[0][j][0], a[RG - 1][j][0], a[0][j][1], a[RG - 1][j][1], b0, b1, T());
-        if constexpr (!I8)
-          mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1], b0, b1, T());
+        mma_16816(d, a[0][j][0], a[RG - 1][j][0], a[0][j][1], a[RG - 1][j][1], b0, b1, bf16());
+        mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1], b0, b1, bf16());
       }
     };
     // v: four tokens of a dimension, 4 or 8 bytes
@@ -702,7 +701,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
     auto load_v = [&](int j, int i, uint32_t* b0, uint32_t* b1) {
       const unsigned char* at = vp + j * 16 * D * Cfg::E + i * 128 * Cfg::E;
       if constexpr (I8) {
-        i8_to_f16(*reinterpret_cast<const uint32_t*>(at), b0, b1);
+        i8_to_bf16(*reinterpret_cast<const uint32_t*>(at), b0, b1);
       } else {
         const uint2 u = *reinterpret_cast<const uint2*>(at);
         *b0 = u.x;
@@ -770,18 +769,20 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       for (int r = 0; r < RG; ++r) {
         float L = l[r] + __shfl_xor_sync(~0u, l[r], 1);
         L += __shfl_xor_sync(~0u, L, 2);
-        L *= kDown;
         const int row = g + 8 * r;
         if (row >= mt->rows) continue;
-        float f = I8 && vref > -INFINITY ? exp2f(vref) * kDown : 1.f;
-        auto value = [&](int i, int k) { return RG == 2 ? o[i][2 * r + k] : o[i][k] + o[i][2 + k]; };
+        float f = I8 ? 64.f : 1.f;
+        const float unit = I8 ? vref : 1.f;
+        if (flags & kWhole) f *= L == 0.f ? 0.f : 1.f / L;
+        auto value = [&](int i, int k) {
+          return (RG == 2 ? o[i][2 * r + k] : o[i][k] + o[i][2 + k]) * f * unit;
+        };
         if (flags & kWhole) {
-          f *= L == 0.f ? 0.f : 1.f / L;
           bf16* op = A.out + mt->b * A.os[0] + mt->h * A.os[1] + (int64_t)(mt->q0 + row) * A.os[2] + 2 * t;
 #pragma unroll
           for (int i = 0; i < kN; ++i)
             *reinterpret_cast<__nv_bfloat162*>(op + 8 * i) =
-                __floats2bfloat162_rn(value(i, 0) * f, value(i, 1) * f);
+                __floats2bfloat162_rn(value(i, 0), value(i, 1));
           if (t == 0)
             A.lse[((int64_t)mt->b * A.C.H + mt->h) * A.S.n + mt->q0 + row] = att_lse(m[r], L);
         } else {
@@ -790,7 +791,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
 #pragma unroll
           for (int i = 0; i < kN; ++i)
             *reinterpret_cast<float2*>(A.part + at * D + 8 * i + 2 * t) =
-                make_float2(value(i, 0) * f, value(i, 1) * f);
+                make_float2(value(i, 0), value(i, 1));
           if (t == 0) *reinterpret_cast<float2*>(A.part_ml + at * 2) = make_float2(m[r], L);
         }
       }

@@ -1,0 +1,115 @@
+"""Rotary positions, the paged cache and attention over it where values, norms and scales lie far
+apart, through the C ABI, against oracle/cache.py (float64).
+
+Tolerances of the attention. With nq the largest ||x_t|| and r the largest ||k_j|| / ||x_j|| (1 but for
+the rounding of a stored row), a logit is a sum of d products, off by d 2^-24 nq r ||x_j||, times
+1 / (||x_j|| sqrt(d)): sqrt(d) 2^-24 nq r; its scalings and its difference to the row's reference are
+six roundings of at most nq r / sqrt(d) <= nq r / 8: together below E = (sqrt(d) + 4) 2^-24 nq r. A weight is
+off by E of itself, 2^-20 for the exponential and 2^-16 for its two bf16 parts; sums of n <= 4096 terms, sixteen
+to a step, by n / 16 2^-23 <= 2^-15 of sum p |v|; the normaliser by as much. The output by
+(2 E + 2^-13) sum p |v| and its own rounding, 2^-8; whatever the sizes of the values in other dimensions, of
+other tokens, or behind the row. lse: E, 2^-14, and 2^-22 of itself.
+"""
+import math
+
+import pytest
+import torch
+
+from lsh_attention_b200 import binding as lb
+from oracle import cache as oc
+from test_gpu_cache import bits, freqs_of, near, randn, same_cache, table_of, to_gpu
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def filled(x, v, page, int8):
+    """A cache of the rows x, v [1, H, n, d], its table, and both on the GPU."""
+    _, H, n, d = x.shape
+    per_seq = n // page + 1
+    ref = oc.empty(per_seq + 1, H, page, d, int8)
+    table = table_of(1, per_seq, per_seq + 1)
+    oc.append(ref, x, v, table, [0])
+    return ref, table, to_gpu(ref)
+
+
+def check_attend(ref, table, gpu, q, length):
+    d = q.shape[-1]
+    out, lse = lb.lsh_cache_attend(gpu, q.cuda(), table.cuda(), ints(length))
+    ro, rl, mag = oc.attend(ref, q, table, [length])
+    r = 1.0
+    for h in range(q.shape[1]):
+        k, _, kinv = oc.read(ref, table, 0, h, length + q.shape[2])
+        r = max(r, float((k.norm(dim=-1) * kinv).max()))
+    E = (math.sqrt(d) + 4) * 2.0 ** -24 * float(q.double().norm(dim=-1).max()) * r
+    near(out, ro, ro.abs() * 2.0 ** -8 + mag * (2 * E + 2.0 ** -13), "out")
+    near(lse, rl, E + 2.0 ** -14 + rl.abs() * 2.0 ** -22, "lse")
+    return out, lse
+
+
+# ------------------------------------------------------------------------------ sizes of values
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 64), (128, 32)])
+@pytest.mark.parametrize("up", [12, 20, 30, 60])
+@pytest.mark.parametrize("where", [3, 397])
+@pytest.mark.parametrize("sharp", [False, True])
+def test_attend_one_large_value(sharp, where, up, d, page, n, int8):
+    """One value of one token is 2^up times the others, with an ordinary weight, or with a small one
+    beside a key that takes nearly all (in whose own zeros the small weights alone are seen): the
+    other dimensions do not feel it."""
+    L = 400
+    x, v = randn(1, 1, L + n, d, seed=1), randn(1, 1, L + n, d, seed=2)
+    if sharp:
+        u = randn(d, seed=3)
+        x[0, 0, L:] = 16 * u + x[0, 0, L:]   # logits of 16 for u, -16 for -u
+        x[0, 0, 200], x[0, 0, where] = u, -u
+        v[0, 0, 200, :d // 2] = 0.0
+    v[0, 0, where, 5] = 2.0 ** up
+    x, v = x.bfloat16(), v.bfloat16()
+    ref, table, gpu = filled(x, v, page, int8)
+    check_attend(ref, table, gpu, x[:, :, L:], L)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n", [4, 13])
+@pytest.mark.parametrize("up", [0, 20, 40, 90])
+def test_attend_a_large_value_behind_the_row(up, n, int8):
+    """The last drafted token begins a page and has large values: the rows before it, which do not
+    see it, are the bits that they are without it."""
+    d, page = 64, 16
+    L = 129 - n
+    x, v = randn(1, 2, L + n, d, seed=1).bfloat16(), randn(1, 2, L + n, d, seed=2).bfloat16()
+    base = None
+    for f in (1.0, 2.0 ** up):
+        w = v.clone()
+        w[:, :, -1] *= f
+        ref, table, gpu = filled(x, w, page, int8)
+        out, lse = check_attend(ref, table, gpu, x[:, :, L:], L)
+        if base is None:
+            base = out, lse
+        assert torch.equal(out[:, :, :-1], base[0][:, :, :-1]) and torch.equal(lse, base[1])
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n", [1, 9])
+@pytest.mark.parametrize("sizes", [(-110,) * 3, (100,) * 3, (0, 30, -30), (-60, 0, 40), (40, -50, 5)])
+def test_attend_values_of_every_size(sizes, n, int8):
+    """Pages of values 2^size, one size after the other, tiny, huge and mixed; the large pages'
+    keys are opposite to the rows where the sizes differ, so that small ones count too."""
+    d, page, L = 64, 32, 500
+    x, v = randn(1, 1, L + n, d, seed=1), randn(1, 1, L + n, d, seed=2)
+    size = torch.tensor(sizes, dtype=torch.float64)[torch.arange(L + n) // page % 3]
+    v = (v.double() * 2.0 ** size[:, None]).bfloat16()
+    if len(set(sizes)) > 1:
+        u = randn(d, seed=3)
+        x[0, 0, L:] += 20 * u
+        x[0, 0, :L] += torch.where((size[:L] == max(sizes))[:, None], -2 * u, 0.0)
+    x = x.bfloat16()
+    ref, table, gpu = filled(x, v, page, int8)
+    check_attend(ref, table, gpu, x[:, :, L:], L)
