@@ -29,13 +29,13 @@
 // of sixteen (calls of more than eight rows) in two.
 //
 // int8: what bounds the kernel besides DRAM is the instructions that widen the
-// bytes. A byte of K becomes the f16 subnormal (q + 128) 2^-24 by being put under
-// a zero (one byte permutation for two); the 128 comes off as -128 sum x, which
-// the product starts from. One of V becomes the bf16 number (q + 128) 2^-133, and by
-// one multiply-add q / 64. Both are exact. Rows of x are f16 scaled by a power of two
-// to a largest value in [2^14, 2^15): exact but for values below 2^-31 of it. A weight
-// is multiplied by its page's scale before it is split: bf16 has the range for it, so
-// that no page's scale costs another page's weights any bits.
+// bytes. One under a zero (a byte permutation for two) is the bf16 number (q + 128) 2^-133,
+// and one multiply-add makes it q / 64, exactly. (Keys fed as f16 subnormals (q + 128) 2^-24,
+// the 128 taken off as -128 sum x, need no multiply-add: 83.1 us instead of 83.7 for the 64
+// images below. But their sums round at the size of 128 sum |x|, whatever the key's:
+// one stored as a few steps of its page's scale, or none, had a logit that was noise.) A
+// weight is multiplied by its page's scale before it is split: bf16 has the range for
+// it, so that no page's scale costs another page's weights any bits.
 //
 // Measured (main kernel / with the joining of parts and both launches), of the copy
 // rate: one token over 65536, 8 heads of 128, bf16: 48.8 us (0.85) / 53; 64 sequences
@@ -48,10 +48,6 @@
 // one copying warp (194); parts joined by the last of eight neighbours, counted
 // with atomics, instead of a second kernel (99: the fences wait for loads under way).
 #pragma once
-
-#include <cuda_fp16.h>
-
-#include <type_traits>
 
 #include "cache.cuh"
 
@@ -102,17 +98,9 @@ struct AttCfg {
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1, bf16) {
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1, __half) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -131,24 +119,13 @@ __device__ __forceinline__ void i8_to_bf16(uint32_t w, uint32_t* b0, uint32_t* b
   *b0 = *reinterpret_cast<const uint32_t*>(&a);
   *b1 = *reinterpret_cast<const uint32_t*>(&b);
 }
-// Four int8 to two pairs of f16 subnormals, (q + 128) 2^-24.
-__device__ __forceinline__ void i8_to_sub(uint32_t w, uint32_t* b0, uint32_t* b1) {
-  w ^= 0x80808080u;
-  *b0 = __byte_perm(w, 0u, 0x4140);
-  *b1 = __byte_perm(w, 0u, 0x4342);
-}
-
-// (x, y) as a pair of T and what the pair leaves over, as another.
+// (x, y) as a pair of bf16 and what the pair leaves over, as another.
 __device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   const __nv_bfloat162 l =
       __floats2bfloat162_rn(x - __bfloat162float(h.x), y - __bfloat162float(h.y));
   *hi = *reinterpret_cast<const uint32_t*>(&h);
   *lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-__device__ __forceinline__ uint32_t pack_h2(float x, float y) {
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -443,7 +420,6 @@ __device__ __forceinline__ float att_lse(float m, float l) {
 template <int D, bool I8, int RG>
 __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(AttendArgs A) {
   using Cfg = AttCfg<D, I8>;
-  using T = std::conditional_t<I8, __half, bf16>;
   constexpr int NG = Cfg::kGroups;
   constexpr int kSteps = D / 16;  // 16-wide steps of Q K^T
   constexpr int kN = D / 8;       // 8-wide column tiles of P V
@@ -475,7 +451,6 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   float o[kN][4];               // eight rows: low parts' sums in the second half
                                 // (int8: in units of 64 vref)
   float m[RG], l[RG];           // a row's reference; sum of this lane's weights
-  float qscale[RG], qbias[RG];  // int8: x is qa * qscale / 2^10; -128 sum qa / 2^24
   // int8: a power of two, a scale of v that was met, and 1 / vref. It is moved only by
   // a scale 2^64 times larger: its purpose is the range alone, any ratio is exact
   float vref = 0.f, vinv = 0.f;
@@ -516,37 +491,12 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
 #pragma unroll
         for (int j = 0; j < D / 32; ++j)
           if (!in) raw[j] = make_uint4(0, 0, 0, 0);
-        if constexpr (I8) {
-          float f[D / 4], top = 0.f, sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) Vec16<bf16>::unpack(raw[j], f + 8 * j);
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(f[i]));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-          // a power of two that brings the row's largest value to [2^14, 2^15)
-          const int e = max(-112, min(126, (int)(__float_as_uint(top) >> 23) - 127));
-          qscale[r] = __uint_as_float((uint32_t)(e + 127) << 23);
-          const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            qa[r][i] = pack_h2(f[2 * i] * up, f[2 * i + 1] * up);
-            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&qa[r][i]));
-            sum += h.x + h.y;
-          }
-          sum += __shfl_xor_sync(~0u, sum, 1);
-          sum += __shfl_xor_sync(~0u, sum, 2);
-          qbias[r] = -sum * 0x1p-17f;
-        } else {
-          qscale[r] = 1.f;
-          qbias[r] = 0.f;
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            qa[r][4 * j] = raw[j].x;
-            qa[r][4 * j + 1] = raw[j].y;
-            qa[r][4 * j + 2] = raw[j].z;
-            qa[r][4 * j + 3] = raw[j].w;
-          }
+        for (int j = 0; j < D / 32; ++j) {
+          qa[r][4 * j] = raw[j].x;
+          qa[r][4 * j + 1] = raw[j].y;
+          qa[r][4 * j + 2] = raw[j].z;
+          qa[r][4 * j + 3] = raw[j].w;
         }
         m[r] = -INFINITY;
         l[r] = 0.f;
@@ -571,7 +521,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
     for (int j = 0; j < NG; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float s[4] = {qbias[0], qbias[0], RG == 2 ? qbias[RG - 1] : 0.f, RG == 2 ? qbias[RG - 1] : 0.f};
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
         const unsigned char* kp = sp + (16 * j + 4 * (g >> 1) + 2 * e + (g & 1)) * D * Cfg::E + 16 * t;
 #pragma unroll
         for (int i = 0; i < D * Cfg::E / 64; ++i) {
@@ -581,15 +531,15 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t b0, b1;
-              i8_to_sub(w[k], &b0, &b1);
+              i8_to_bf16(w[k], &b0, &b1);
               const int a = 2 * (4 * i + k);
-              mma_16816(s, q_of(0, a), q_of(1, a), q_of(0, a + 1), q_of(1, a + 1), b0, b1, T());
+              mma_16816(s, q_of(0, a), q_of(1, a), q_of(0, a + 1), q_of(1, a + 1), b0, b1);
             }
           } else {
             mma_16816(s, q_of(0, 4 * i), q_of(1, 4 * i), q_of(0, 4 * i + 1), q_of(1, 4 * i + 1), u.x,
-                      u.y, T());
+                      u.y);
             mma_16816(s, q_of(0, 4 * i + 2), q_of(1, 4 * i + 2), q_of(0, 4 * i + 3),
-                      q_of(1, 4 * i + 3), u.z, u.w, T());
+                      q_of(1, 4 * i + 3), u.z, u.w);
           }
         }
 #pragma unroll
@@ -607,12 +557,13 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
       if constexpr (I8) vtop = fmaxf(vtop, mt->vs[j]);
 #pragma unroll
       for (int r = 0; r < RG; ++r) {
-        float f = cs;
-        if constexpr (I8) f *= mt->ks[j] * 1024.f * qscale[r];
-        p[r][j][0] *= kn.x * f;
-        p[r][j][1] *= kn.y * f;
-        p[r][j][2] *= kn.z * f;
-        p[r][j][3] *= kn.w * f;
+        // (int8: the product with the key as it stands first: 1/||x_j|| times the scale may
+        // overflow where the key is stored as zeros)
+        const float f = I8 ? cs * 64.f * mt->ks[j] : cs;
+        p[r][j][0] = I8 ? p[r][j][0] * f * kn.x : p[r][j][0] * (kn.x * f);
+        p[r][j][1] = I8 ? p[r][j][1] * f * kn.y : p[r][j][1] * (kn.y * f);
+        p[r][j][2] = I8 ? p[r][j][2] * f * kn.z : p[r][j][2] * (kn.z * f);
+        p[r][j][3] = I8 ? p[r][j][3] * f * kn.w : p[r][j][3] * (kn.w * f);
       }
     }
     // units with tokens that some row must not see, or that are not there
@@ -690,10 +641,10 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
     // d += P V of group j's tokens for one tile of dimensions
     auto product = [&](float (&d)[4], int j, uint32_t b0, uint32_t b1) {
       if constexpr (RG == 1) {
-        mma_16816(d, a[0][j][0], al[0][j][0], a[0][j][1], al[0][j][1], b0, b1, bf16());
+        mma_16816(d, a[0][j][0], al[0][j][0], a[0][j][1], al[0][j][1], b0, b1);
       } else {
-        mma_16816(d, a[0][j][0], a[RG - 1][j][0], a[0][j][1], a[RG - 1][j][1], b0, b1, bf16());
-        mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1], b0, b1, bf16());
+        mma_16816(d, a[0][j][0], a[RG - 1][j][0], a[0][j][1], a[RG - 1][j][1], b0, b1);
+        mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1], b0, b1);
       }
     };
     // v: four tokens of a dimension, 4 or 8 bytes

@@ -8,7 +8,8 @@ six roundings of at most nq r / sqrt(d) <= nq r / 8: together below E = (sqrt(d)
 off by E of itself, 2^-20 for the exponential and 2^-16 for its two bf16 parts; sums of n <= 4096 terms, sixteen
 to a step, by n / 16 2^-23 <= 2^-15 of sum p |v|; the normaliser by as much. The output by
 (2 E + 2^-13) sum p |v| and its own rounding, 2^-8; whatever the sizes of the values in other dimensions, of
-other tokens, or behind the row. lse: E, 2^-14, and 2^-22 of itself.
+other tokens, or behind the row. lse: E, 2^-14, and 2^-22 of itself. Both formats: the bounds of
+test_gpu_cache.py for int8 are wider, derived for weights in f16 and keys with an offset.
 """
 import math
 
@@ -78,12 +79,13 @@ def test_attend_one_large_value(sharp, where, up, d, page, n, int8):
 
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("n", [4, 13])
+@pytest.mark.parametrize("end", [113, 129])
 @pytest.mark.parametrize("up", [0, 20, 40, 90])
-def test_attend_a_large_value_behind_the_row(up, n, int8):
+def test_attend_a_large_value_behind_the_row(up, end, n, int8):
     """The last drafted token begins a page and has large values: the rows before it, which do not
     see it, are the bits that they are without it."""
     d, page = 64, 16
-    L = 129 - n
+    L = end - n
     x, v = randn(1, 2, L + n, d, seed=1).bfloat16(), randn(1, 2, L + n, d, seed=2).bfloat16()
     base = None
     for f in (1.0, 2.0 ** up):
@@ -112,4 +114,29 @@ def test_attend_values_of_every_size(sizes, n, int8):
         x[0, 0, :L] += torch.where((size[:L] == max(sizes))[:, None], -2 * u, 0.0)
     x = x.bfloat16()
     ref, table, gpu = filled(x, v, page, int8)
+    check_attend(ref, table, gpu, x[:, :, L:], L)
+
+
+@pytest.mark.parametrize("n", [1, 12])
+@pytest.mark.parametrize("d,page", [(64, 16), (64, 128), (128, 32)])
+@pytest.mark.parametrize("up", [4, 10, 16, 24, 60])
+def test_attend_short_rows_beside_a_long_one(up, d, page, n):
+    """int8 rows far shorter than the longest of their page are stored as a few steps of its scale or
+    none; their logits are those of what is stored, 0 where that is nothing."""
+    L = 300
+    x, v = randn(1, 2, L + n, d, seed=1), randn(1, 2, L + n, d, seed=2)
+    x[:, :, 5:L:page] *= 2.0 ** up
+    x, v = x.bfloat16(), v.bfloat16()
+    ref, table, gpu = filled(x, v, page, True)
+    check_attend(ref, table, gpu, x[:, :, L:], L)
+
+
+def test_attend_a_tiny_row_beside_a_huge_one():
+    """1/||x|| and the page's scale, both near the ends of fp32: the tiny row is stored as zeros."""
+    d, page, L = 64, 16, 100
+    x, v = randn(1, 1, L + 1, d, seed=1), randn(1, 1, L + 1, d, seed=2)
+    x[0, 0, 20] *= 2.0 ** 90
+    x[0, 0, 21] *= 2.0 ** -120
+    x, v = x.bfloat16(), v.bfloat16()
+    ref, table, gpu = filled(x, v, page, True)
     check_attend(ref, table, gpu, x[:, :, L:], L)
