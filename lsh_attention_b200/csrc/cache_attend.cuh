@@ -128,6 +128,12 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t*
   *lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+// A pair of bf16 with what is not finite set to zero.
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  const __nv_bfloat162 most = __bfloat162bfloat162(__ushort_as_bfloat16(0x7f7f));
+  return w & __hle2_mask(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)), most);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -638,13 +644,15 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
           split2(p[r][j][2 * e], p[r][j][2 * e + 1], &a[r][j][e], &al[r][j][e]);
       }
     }
-    // d += P V of group j's tokens for one tile of dimensions
+    // d += P V of group j's tokens for one tile of dimensions. An infinite or NaN
+    // value counts with the weights' high parts alone: low ones are zeros or of either sign
     auto product = [&](float (&d)[4], int j, uint32_t b0, uint32_t b1) {
       if constexpr (RG == 1) {
         mma_16816(d, a[0][j][0], al[0][j][0], a[0][j][1], al[0][j][1], b0, b1);
       } else {
         mma_16816(d, a[0][j][0], a[RG - 1][j][0], a[0][j][1], a[RG - 1][j][1], b0, b1);
-        mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1], b0, b1);
+        mma_16816(d, al[0][j][0], al[RG - 1][j][0], al[0][j][1], al[RG - 1][j][1],
+                  I8 ? b0 : finite2(b0), I8 ? b1 : finite2(b1));
       }
     };
     // v: four tokens of a dimension, 4 or 8 bytes
@@ -726,7 +734,9 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
         const float unit = I8 ? vref : 1.f;
         if (flags & kWhole) f *= L == 0.f ? 0.f : 1.f / L;
         auto value = [&](int i, int k) {
-          return (RG == 2 ? o[i][2 * r + k] : o[i][k] + o[i][2 + k]) * f * unit;
+          float y = o[i][2 * r + k];
+          if (RG == 1 && fabsf(y) < INFINITY) y += o[i][2 + k];  // (low parts, as in product)
+          return y * f * unit;
         };
         if (flags & kWhole) {
           bf16* op = A.out + mt->b * A.os[0] + mt->h * A.os[1] + (int64_t)(mt->q0 + row) * A.os[2] + 2 * t;

@@ -140,3 +140,35 @@ def test_attend_a_tiny_row_beside_a_huge_one():
     x, v = x.bfloat16(), v.bfloat16()
     ref, table, gpu = filled(x, v, page, True)
     check_attend(ref, table, gpu, x[:, :, L:], L)
+
+
+@pytest.mark.parametrize("n", [1, 5, 12])
+@pytest.mark.parametrize("d,L", [(64, 40), (64, 5000), (128, 300)])
+def test_attend_sees_infinite_values(d, L, n):
+    """Infinite values that a row sees, early, in the middle and among the new tokens: its sum is
+    infinite with their sign, NaN where signs differ or a value is NaN; other dimensions and rows
+    before them are as ever."""
+    page = 32
+    x, v = randn(1, 2, L + n, d, seed=1).bfloat16(), randn(1, 2, L + n, d, seed=2).bfloat16()
+    v[0, 0, 3, 7] = math.inf
+    v[0, 0, L // 2, 8] = -math.inf
+    v[0, 0, 2, 9], v[0, 0, L // 2, 9] = math.inf, -math.inf
+    v[0, 0, 4, 10] = math.nan
+    v[0, 1, L, 11] = math.inf
+    v[0, 1, L + n - 1, 12] = -math.inf
+    ref, table, gpu = filled(x, v, page, False)
+    out, _ = lb.lsh_cache_attend(gpu, x[:, :, L:].cuda(), table.cuda(), ints(L))
+    clean = torch.where(torch.isfinite(v), v, 0.0)
+    ref, _, gpu = filled(x, clean, page, False)
+    check_attend(ref, table, gpu, x[:, :, L:], L)
+    want, _, mag = oc.attend(ref, x[:, :, L:], table, [L])
+    # a token's own weight, exp(-1e5), is 0: 0 times infinity is NaN
+    want[0, 0, :, 7], want[0, 0, :, 8] = math.inf, -math.inf
+    want[0, 0, :, 9] = want[0, 0, :, 10] = math.nan
+    want[0, 1, 0, 11], want[0, 1, 1:, 11] = math.nan, math.inf
+    want[0, 1, n - 1, 12] = math.nan
+    assert torch.equal(torch.isnan(out.cpu()), torch.isnan(want))
+    live = ~torch.isnan(want)
+    want, mag = want[live], mag[live]
+    # E, with ||x|| < 16, is below 2^-15
+    near(out.cpu()[live], want, torch.where(torch.isinf(want), 0.0, want.abs()) * 2.0 ** -8 + mag * 2.0 ** -12, "out")
