@@ -68,12 +68,12 @@ struct AttendArgs {
   int4* rec;       // [B][H][groups]: first warp, how many share it (0: it is whole), rows
 };
 
-// A ring stage's header, written by the copying warp.
+// A ring stage's header, written by the copying warp and handed over by a barrier of
+// its own (`head`): it is read while the unit's tokens still travel.
 struct UnitMeta {
   int b, h, q0, rows;   // the segment's first row and how many
   int len, t0;          // tokens before the sequence's rows; the unit's first
   int flags, slot;      // kFirst ...; slot of a partial result
-  int n;                // the unit's number in the warp's run
   uint32_t ok;          // bit s: tokens 16 s .. of the unit are there
   float ks[4], vs[4];   // int8: scales of k and v
 };
@@ -94,7 +94,8 @@ struct AttCfg {
   static constexpr int kDepth = D == 64 ? 2 : 3;
   static constexpr int kCopy = 4;                   // copying warps
   static constexpr int kThreads = 32 * (kWarps + kCopy);
-  static constexpr int kSmem = 512 + kWarps * kDepth * kStage;
+  static constexpr int kBars = 768;                 // full, empty and head, 32 each
+  static constexpr int kSmem = kBars + kWarps * kDepth * kStage;
 };
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -171,7 +172,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 // lane 4 q + s the tokens 16 s .. of its units. The lane groups go their own ways.
 template <int D, bool I8, int RG>
 __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64_t* full,
-                              uint64_t* empty, int pw) {
+                              uint64_t* empty, uint64_t* head, int pw) {
   using Cfg = AttCfg<D, I8>;
   constexpr int NG = Cfg::kGroups, kServe = Cfg::kWarps / Cfg::kCopy;
   const CacheView& C = A.C;
@@ -260,7 +261,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
   };
   Unit cur, nxt;
   float ks = 0.f, vs = 0.f;
-  bool head = false, starts = true;  // the warp has the segment's first unit; a run or segment starts
+  bool begun = false, starts = true;  // the warp has the segment's first unit; a run or segment starts
   auto walk = [&](Unit& k) {
     k.flags = kEnd;
     k.id = -1;
@@ -268,8 +269,8 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
     const int q0 = grp * 8 * RG, rows = min(8 * RG, nv - q0);
     if (unit == 0) starts = true;
     if (starts) {
-      head = unit == 0;
-      if (head && sl == 0) {
+      begun = unit == 0;
+      if (begun && sl == 0) {
         int4 r = make_int4(run, 0, rows, 0);
         if (units > left)  // it goes on in the runs behind: up to which
           r.y = run_of(u + units - 1) - run + 1;
@@ -283,8 +284,8 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
     k.rows = rows;
     k.len = len;
     k.t0 = unit * Cfg::kTok;
-    k.flags = (starts ? kFirst : 0) | (ends || left == 1 ? kLast : 0) | (ends && head ? kWhole : 0);
-    k.slot = head;
+    k.flags = (starts ? kFirst : 0) | (ends || left == 1 ? kLast : 0) | (ends && begun ? kWhole : 0);
+    k.slot = begun;
     starts = false;
     const int pos = k.t0 + 16 * sl;
     if (sl < NG && pos < len + q0 + rows) {
@@ -319,7 +320,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
   walk(nxt);
   scales(cur);
 
-  int st = 0, n = 0;
+  int st = 0;
   uint32_t ph = 0;
   bool open = q < kServe;  // an end has still to be sent
   const int chunk = min(C.P / 16, NG);  // groups that lie together in a page
@@ -333,6 +334,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
       continue;
     }
     if (go) {
+      __syncwarp(mine);  // one lane has seen the stage free, four write to it
       unsigned char* sp = stages + (size_t)slot * Cfg::kStage;
       UnitMeta* mt = reinterpret_cast<UnitMeta*>(sp + Cfg::kMeta);
       const uint32_t ok = (__ballot_sync(mine, cur.id >= 0) >> (4 * q)) & 15;
@@ -354,7 +356,7 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
       __syncwarp(mine);
       if (sl == 0) {
         sm100::mbar_expect_tx(&full[slot], __popc(ok) * (32 * D * Cfg::E + 64));
-        *reinterpret_cast<volatile int*>(&mt->n) = n;
+        sm100::mbar_arrive(&head[slot]);
       }
       __syncwarp(mine);
       if (cur.id >= 0) {
@@ -377,7 +379,6 @@ __device__ void att_copy_warp(const AttendArgs& A, unsigned char* stages, uint64
       cur = nxt;
       scales(cur);
       walk(nxt);
-      ++n;
       if (++st == Cfg::kDepth) {
         st = 0;
         ph ^= 1;
@@ -432,7 +433,8 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   extern __shared__ __align__(16) unsigned char smem[];
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
   uint64_t* empty = full + 32;
-  unsigned char* stages = smem + 512;
+  uint64_t* head = full + 64;
+  unsigned char* stages = smem + Cfg::kBars;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
   // k_cache_combine may be brought in where there is room: it waits for our end
@@ -440,12 +442,12 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   if (threadIdx.x < Cfg::kWarps * Cfg::kDepth) {
     sm100::mbar_init(&full[threadIdx.x], 1);
     sm100::mbar_init(&empty[threadIdx.x], 1);
-    reinterpret_cast<UnitMeta*>(stages + (size_t)threadIdx.x * Cfg::kStage + Cfg::kMeta)->n = -1;
+    sm100::mbar_init(&head[threadIdx.x], 1);
     sm100::fence_mbar_init();
   }
   __syncthreads();
   if (warp >= Cfg::kWarps) {
-    att_copy_warp<D, I8, RG>(A, stages, full, empty, warp - Cfg::kWarps);
+    att_copy_warp<D, I8, RG>(A, stages, full, empty, head, warp - Cfg::kWarps);
     return;
   }
   att_pad_rows<D, Cfg::kWarps * 32, 8 * RG>(A);
@@ -463,22 +465,14 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
   int st = 0;
   uint32_t ph = 0;
 
-  for (int n = 0;; ++n) {
+  for (;;) {
     const int slot = warp * Cfg::kDepth + st;
     const unsigned char* sp = stages + (size_t)slot * Cfg::kStage;
     const UnitMeta* mt = reinterpret_cast<const UnitMeta*>(sp + Cfg::kMeta);
     // the header is there once the unit is issued: a new segment's rows are
     // fetched while its first tokens travel
-    bool late = false;
-    for (uint64_t t0 = 0; *reinterpret_cast<const volatile int*>(&mt->n) != n && !late;) {
-      __nanosleep(20);
-      const uint64_t now = sm100::global_ns();
-      if (t0 == 0) t0 = now;
-      late = now - t0 > sm100::kWaitLimitNs;
-    }
-    if (__any_sync(~0u, late)) break;
-    __syncwarp();  // the header's other fields are read behind its number
-    const int flags = *reinterpret_cast<const volatile int*>(&mt->flags);
+    if (__any_sync(~0u, !sm100::mbar_wait(&head[slot], ph))) break;
+    const int flags = mt->flags;
     if (flags & kEnd) break;
     if (flags & kFirst) {
 #pragma unroll
@@ -513,10 +507,7 @@ __global__ void __launch_bounds__(AttCfg<D, I8>::kThreads, 1) k_cache_attend(Att
         for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
       vref = vinv = 0.f;
     }
-    if (__any_sync(~0u, !sm100::mbar_wait(&full[slot], ph))) {
-      late = true;
-      break;
-    }
+    if (__any_sync(~0u, !sm100::mbar_wait(&full[slot], ph))) break;
 
     // S, two tiles of eight tokens for each group of 16: column c of tile e is the
     // group's token 4 (c / 2) + 2 e + c % 2, so that this lane holds its tokens
