@@ -417,7 +417,8 @@ typedef struct {
  * 127 s covers its rows' finite values; a row that raises it has the earlier
  * rows of the page rounded again from what is stored, q' = rint(q s / s').
  * The first row of a page sets its scale afresh. Infinities are stored as
- * +-127 s, NaN as 0, and recorded in the status.
+ * +-127 s, NaN as 0, and recorded in the status; a row of x that has one gets
+ * key_inv_norm 0, so that its logits are 0 and it spoils no other token.
  * A page that is written must belong to one sequence of the call and stand in
  * its table once; a prefix that several sequences share may be read by all. */
 lsh_status lsh_cache_append(const lsh_cache_desc *desc, const lsh_cache *cache,

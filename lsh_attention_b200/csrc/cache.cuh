@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D,
       const int pg = r >> pshift, id = ids[pg];
       // the row's slot in its page (page_base of id: [P][D] a head)
       const int64_t at = ((int64_t)id * C.H + h) * C.P + ((off0 + r) & pmask);
-      if (in && id >= 0 && dim0 == 0) C.kinv[at] = inv;
+      // int8 stores NaN as 0: the row's logits are 0 then, as an infinite row's are
+      if (in && id >= 0 && dim0 == 0) C.kinv[at] = I8 && inv != inv ? 0.f : inv;
       if constexpr (TURN != kTurnNone) {
         float y[8], c[P8::kPairs], s[P8::kPairs];
         if constexpr (ADJ) {

@@ -100,7 +100,8 @@ def append(cache, rows, v, page_table, seq_len, n_valid=None, x=None):
                 p = first + t
                 page, slot = int(page_table[b, p // P]), p % P
                 norm = float(x[b, h, t].double().norm())
-                cache["key_inv_norm"][page, h, slot] = 0.0 if norm < TINY else 1.0 / norm
+                none = norm < TINY or (cache["k_scale"] is not None and math.isnan(norm))
+                cache["key_inv_norm"][page, h, slot] = 0.0 if none else 1.0 / norm
                 if cache["k_scale"] is None:
                     cache["k"][page, h, slot] = rows[b, h, t]
                     _v_row(cache, page, h, slot).copy_(v[b, h, t])

@@ -172,3 +172,26 @@ def test_attend_sees_infinite_values(d, L, n):
     want, mag = want[live], mag[live]
     # E, with ||x|| < 16, is below 2^-15
     near(out.cpu()[live], want, torch.where(torch.isinf(want), 0.0, want.abs()) * 2.0 ** -8 + mag * 2.0 ** -12, "out")
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("page", [16, 64])
+def test_append_of_a_row_that_is_not_finite(page, bad):
+    """int8: such a row counts with 1/||x|| = 0, as its logit does, and spoils no other token."""
+    d, L = 64, 40
+    x, v = randn(1, 2, L + 1, d, seed=1).bfloat16(), randn(1, 2, L + 1, d, seed=2).bfloat16()
+    x[0, 1, 11, 6] = bad
+    x[0, 0, 23, 0], x[0, 0, 23, 1] = bad, 3.0
+    ref, table, _ = filled(x, v, page, True)
+    gpu = to_gpu(oc.empty(ref["k"].shape[0], 2, page, d, True))
+    lb.lsh_cache_append(gpu, x.cuda(), v.cuda(), table.cuda(), ints(0))
+    same_cache(gpu, ref)
+    for h, t in ((1, 11), (0, 23)):
+        assert float(gpu.key_inv_norm[int(table[0, t // page]), h, t % page]) == 0.0
+    check_attend(ref, table, gpu, x[:, :, L:], L)
+    assert gpu.get_device_status() == 6
+    # a bf16 cache holds the row as it is
+    ref, table, gpu = filled(x, v, page, False)
+    gpu = to_gpu(oc.empty(ref["k"].shape[0], 2, page, d, False))
+    lb.lsh_cache_append(gpu, x.cuda(), v.cuda(), table.cuda(), ints(0))
+    same_cache(gpu, ref)
