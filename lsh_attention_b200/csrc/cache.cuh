@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(256) k_cache_gather(GatherArgs A) {
   bf16* xo = A.x + b * A.xs[0] + h * A.xs[1];
   bf16* vo = A.v + b * A.vs[0] + h * A.vs[1];
   int id = -1;
-  if (i0 < nv) {
+  if (max(i0, 0) < nv) {  // a sequence without rows has no group, wherever it starts
     id = page_of(C, A.S, b, (int)(at / C.P));
     if (id < 0 && lane == 0) cache_error(C);
   }

@@ -195,3 +195,22 @@ def test_append_of_a_row_that_is_not_finite(page, bad):
     gpu = to_gpu(oc.empty(ref["k"].shape[0], 2, page, d, False))
     lb.lsh_cache_append(gpu, x.cuda(), v.cuda(), table.cuda(), ints(0))
     same_cache(gpu, ref)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_gather_of_no_rows_looks_at_no_page(int8):
+    """A sequence that sits a read-back out: its page numbers do not count, wherever it starts."""
+    d, page, H = 64, 16, 2
+    ref = oc.empty(3, H, page, d, int8, fill=0.5)
+    gpu = to_gpu(ref)
+    table = torch.tensor([[1, 2], [-1, -1], [-5, 10 ** 6]], dtype=torch.int32)
+    x, v = lb.lsh_cache_gather(gpu, table.cuda(), ints(3, 3, 19), 5, n_valid=ints(5, 0, 0))
+    assert gpu.get_device_status() == 0
+    assert (x[1:] == 0).all() and (v[1:] == 0).all()
+    # nor does a page in front of the rows
+    table[1] = torch.tensor([-1, 0])
+    lb.lsh_cache_gather(gpu, table.cuda(), ints(3, 17, 16), 5, n_valid=ints(5, 2, 0))
+    assert gpu.get_device_status() == 0
+    table[1, 1] = -1
+    lb.lsh_cache_gather(gpu, table.cuda(), ints(3, 17, 16), 5, n_valid=ints(5, 2, 0))
+    assert gpu.get_device_status() == 6
