@@ -414,9 +414,12 @@ typedef struct {
  * unless NULL, receives the rotated rows (the queries of lsh_cache_attend),
  * zeros past n_valid. Slots of other tokens are left as they are.
  * int8: a page's scale is the smallest power of two s >= 2^-126 such that
- * 127 s covers its rows' finite values; a row that raises it has the earlier
- * rows of the page rounded again from what is stored, q' = rint(q s / s').
- * The first row of a page sets its scale afresh. Infinities are stored as
+ * 127 s covers the finite values of the rows it was given since its first; rows
+ * that raise it have the earlier rows of the page rounded again from what is
+ * stored, q' = rint(q s / s'). The first row of a page sets its scale afresh;
+ * while a page holds earlier rows, its scale never falls. So rows that are
+ * overwritten later (drafted ones, by a call with a smaller seq_len) count in the
+ * scale and in the rounding of those before them for good. Infinities are stored as
  * +-127 s, NaN as 0, and recorded in the status; a row of x that has one gets
  * key_inv_norm 0, so that its logits are 0 and it spoils no other token.
  * A page that is written must belong to one sequence of the call and stand in

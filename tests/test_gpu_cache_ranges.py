@@ -214,3 +214,28 @@ def test_gather_of_no_rows_looks_at_no_page(int8):
     table[1, 1] = -1
     lb.lsh_cache_gather(gpu, table.cuda(), ints(3, 17, 16), 5, n_valid=ints(5, 2, 0))
     assert gpu.get_device_status() == 6
+
+
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("at", [0, 5, 15, 20])
+def test_append_again_behind_rejected_rows(at, d, page):
+    """Drafted rows, one of them large, appended, rejected and overwritten: a scale does not fall
+    while its page holds earlier rows, which stay as they were rounded; with none it starts afresh."""
+    H, n = 2, 7
+    table = table_of(1, 3, 4)
+    ref = oc.empty(4, H, page, d, True)
+    gpu = to_gpu(ref)
+    x, v = (randn(1, H, at + n, d, seed=s).bfloat16() for s in (1, 2))
+    big = [t.clone() for t in (x, v)]
+    for t in big:
+        t[0, :, at + 2] *= 64.0
+    calls = [(x[:, :, :at], v[:, :, :at], 0)] if at else []
+    calls += [(t[0][:, :, at:at + m], t[1][:, :, at:at + m], at) for t, m in ((big, n), ((x, v), 3), (big, 2))]
+    for a, b, start in calls:
+        oc.append(ref, a, b, table, [start])
+        lb.lsh_cache_append(gpu, a.cuda(), b.cuda(), table.cuda(), ints(start))
+        same_cache(gpu, ref)
+    if at % page and (at + 2) // page == at // page:
+        stored = oc.read(ref, table, 0, 0, at)[0]
+        err = (stored - x[0, 0, :at].double()).abs().amax()
+        assert float(err) > 64 * 2.0 ** -7  # the rejected row's scale is what they are rounded to
