@@ -320,10 +320,11 @@ lsh_status lsh_topk_forward(const lsh_topk_desc *desc, const void *x, const void
  *     position); the d values of a row are contiguous. Row pointers are
  *     16-byte aligned and strides multiples of 16 bytes, so both
  *     [B][H][n][d] and the projections' [B][n][H][d] are read in place.
- *     Strides of inputs may be 0 (one row for all); written rows must not
- *     overlap (LSH_ERR_INVALID_ARG). Limits (else LSH_ERR_UNSUPPORTED): n, the
- *     rows of a sequence, and the batch of lsh_rope 2^24; heads and the
- *     batches of the cache's calls 65535; max_pages * page_size 2^31 - 2^24.
+ *     Strides of inputs may be 0 (one row for all), no axis may step further than
+ *     2^59 elements, and written rows must not overlap (LSH_ERR_INVALID_ARG).
+ *     Limits (else LSH_ERR_UNSUPPORTED): n, the rows of a sequence, and the
+ *     batch of lsh_rope 2^24; heads and the batches of the cache's calls 65535;
+ *     max_pages * page_size 2^31 - 2^24.
  *   - Lengths, page numbers and positions are read on the device: a captured
  *     graph may be replayed after they change.
  *   - Nothing is allocated and no call synchronises.

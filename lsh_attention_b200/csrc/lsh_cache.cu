@@ -24,10 +24,14 @@ inline lsh_status last_cuda() {
 }
 
 // Rows [B][H][n] of d contiguous elements: strides non-negative multiples of
-// 16 bytes, small enough that no byte offset leaves 63 bits.
-bool strides_ok(const int64_t (&s)[3], int esize) {
-  for (int64_t v : s)
-    if (v < 0 || v * esize % 16 != 0 || v >= (int64_t(1) << 44)) return false;
+// 16 bytes, and no axis steps further than 2^59 elements, so that sums of offsets in
+// bytes stay below 2^63.
+bool strides_ok(const int64_t (&s)[3], int B, int H, int n, int esize) {
+  const int64_t count[3] = {B, H, n};
+  for (int i = 0; i < 3; ++i)
+    if (s[i] < 0 || s[i] >= (int64_t(1) << 44) || s[i] * esize % 16 != 0 ||
+        s[i] > (int64_t(1) << 59) / std::max<int64_t>(1, count[i] - 1))
+      return false;
   return true;
 }
 
@@ -262,7 +266,8 @@ lsh_status lsh_rope(const lsh_rope_desc* desc, const void* x, const int32_t* pos
   if (!x || !positions || !freqs || !out || !aligned16(x) || !aligned16(out))
     return LSH_ERR_INVALID_ARG;
   const int esize = q.dtype == LSH_BF16 ? 2 : 4;
-  if (!strides_ok(q.x_stride, esize) || !strides_ok(q.out_stride, esize) ||
+  if (!strides_ok(q.x_stride, q.batch, q.heads, q.n, esize) ||
+      !strides_ok(q.out_stride, q.batch, q.heads, q.n, esize) ||
       !rows_apart(q.out_stride, q.batch, q.heads, q.n, q.d))
     return LSH_ERR_INVALID_ARG;
   A.pos = positions;
@@ -297,8 +302,9 @@ lsh_status lsh_cache_append(const lsh_cache_desc* desc, const lsh_cache* cache,
   if (!x || !v || !aligned16(x) || !aligned16(v) || !aligned16(xr)) return LSH_ERR_INVALID_ARG;
   if (A.rot.axes > 0 && (!positions || !freqs)) return LSH_ERR_INVALID_ARG;
   if (rows->pos_batched != 0 && rows->pos_batched != 1) return LSH_ERR_INVALID_ARG;
-  if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->v_stride, 2) ||
-      (xr && (!strides_ok(rows->out_stride, 2) ||
+  if (!strides_ok(rows->x_stride, A.S.B, A.C.H, A.S.n, 2) ||
+      !strides_ok(rows->v_stride, A.S.B, A.C.H, A.S.n, 2) ||
+      (xr && (!strides_ok(rows->out_stride, A.S.B, A.C.H, A.S.n, 2) ||
               !rows_apart(rows->out_stride, A.S.B, A.C.H, A.S.n, A.C.d))))
     return LSH_ERR_INVALID_ARG;
   A.x = static_cast<const __nv_bfloat16*>(x);
@@ -336,7 +342,8 @@ lsh_status lsh_cache_gather(const lsh_cache_desc* desc, const lsh_cache* cache,
   lsh_status s = check_cache(desc, cache, rows, page_table, start, n_valid, &A.C, &A.S);
   if (s != LSH_OK) return s;
   if (!x || !v || !aligned16(x) || !aligned16(v)) return LSH_ERR_INVALID_ARG;
-  if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->v_stride, 2) ||
+  if (!strides_ok(rows->x_stride, A.S.B, A.C.H, A.S.n, 2) ||
+      !strides_ok(rows->v_stride, A.S.B, A.C.H, A.S.n, 2) ||
       !rows_apart(rows->x_stride, A.S.B, A.C.H, A.S.n, A.C.d) ||
       !rows_apart(rows->v_stride, A.S.B, A.C.H, A.S.n, A.C.d))
     return LSH_ERR_INVALID_ARG;
@@ -376,7 +383,8 @@ lsh_status lsh_cache_attend(const lsh_cache_desc* desc, const lsh_cache* cache,
   lsh_status s = check_cache(desc, cache, rows, page_table, seq_len, n_valid, &A.C, &A.S);
   if (s != LSH_OK) return s;
   if (!x || !out || !lse || !aligned16(x) || !aligned16(out)) return LSH_ERR_INVALID_ARG;
-  if (!strides_ok(rows->x_stride, 2) || !strides_ok(rows->out_stride, 2) ||
+  if (!strides_ok(rows->x_stride, A.S.B, A.C.H, A.S.n, 2) ||
+      !strides_ok(rows->out_stride, A.S.B, A.C.H, A.S.n, 2) ||
       !rows_apart(rows->out_stride, A.S.B, A.C.H, A.S.n, A.C.d))
     return LSH_ERR_INVALID_ARG;
   const AttendLayout L = attend_layout(*desc, *rows);
