@@ -239,3 +239,18 @@ def test_append_again_behind_rejected_rows(at, d, page):
         stored = oc.read(ref, table, 0, 0, at)[0]
         err = (stored - x[0, 0, :at].double()).abs().amax()
         assert float(err) > 64 * 2.0 ** -7  # the rejected row's scale is what they are rounded to
+
+
+def test_rope_fp32_sines():
+    """Rows (1, 0): the sines and cosines themselves. The angle's fraction of a turn is off by
+    2 * 2^-32, 2^-28 in the angle; a sine by a step, at most 2^-24, and by the rounding of a sum, 2^-25.
+    Together below 2^-23.3."""
+    n, d = 40000, 64
+    x = torch.zeros(1, 1, n, d)
+    x[..., :32] = 1.0
+    pos = torch.arange(n, dtype=torch.int32)[None] * 53
+    f = freqs_of((64,))
+    out = lb.lsh_rope(x.cuda(), pos.cuda(), f.cuda(), axis_dims=(64,))
+    t = pos[0, :, None].double() * f.double()
+    want = torch.cat([t.cos(), t.sin()], -1)[None, None]
+    near(out, want, 2.0 ** -23.3, "sines")
