@@ -357,8 +357,8 @@ typedef struct {
  * their precision; the rotation is fp32 and rounds once. inverse = 1 is the
  * gradient with respect to x (and undoes the call). Sines and cosines of bf16
  * rows are good to 2^-21, of fp32 rows to 2^-23. positions int32, any sign;
- * freqs [sum dims / 2] fp32. out may be x itself with the same strides, else
- * they must not overlap. */
+ * freqs [sum dims / 2] fp32, any sign, at most 2^45 in size. out may be x
+ * itself with the same strides, else they must not overlap. */
 lsh_status lsh_rope(const lsh_rope_desc *desc, const void *x, const int32_t *positions,
                     const float *freqs, void *out, void *stream);
 

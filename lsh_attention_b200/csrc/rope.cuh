@@ -33,12 +33,15 @@ __device__ __forceinline__ int rot_axis(const RotPlan& r, int p) {
 }
 
 // A frequency, radians a position, as a fraction of a turn in units of 2^-64.
-// 1 / (2 pi) is taken to 107 bits, so that the product is good to 2^-64.
+// 1 / (2 pi) is taken to 107 bits, so that the product is good to 2^-63 for frequencies
+// up to 2^45. That of a negative one is the negative of its opposite's: its own
+// distance from the next lower turn would keep 53 bits.
 __device__ __forceinline__ uint2 rot_phase(float freq) {
-  const double f = (double)freq, hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  const double f = fabs((double)freq), hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
   const double p = f * hi, e = fma(f, hi, -p) + f * lo;
   // the fraction of p in [0, 1) has 53 bits; what is left of p is below 2^-53 of it
-  const uint64_t u = (uint64_t)((p - floor(p)) * 0x1p64) + (uint64_t)(int64_t)(e * 0x1p64);
+  uint64_t u = (uint64_t)((p - floor(p)) * 0x1p64) + (uint64_t)(int64_t)(e * 0x1p64);
+  if (freq < 0.f) u = 0 - u;
   return make_uint2((uint32_t)u, (uint32_t)(u >> 32));
 }
 

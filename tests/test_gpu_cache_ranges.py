@@ -254,3 +254,19 @@ def test_rope_fp32_sines():
     t = pos[0, :, None].double() * f.double()
     want = torch.cat([t.cos(), t.sin()], -1)[None, None]
     near(out, want, 2.0 ** -23.3, "sines")
+
+
+def test_rope_negative_frequencies_at_far_positions():
+    """A frequency and its negative turn to the same angle, as exactly: angles of positions up to
+    2^31, whose fraction of a turn is off by 2 * 2^-32, sines to 2^-24 and a rounding each."""
+    d, n = 64, 64
+    g = torch.Generator().manual_seed(1)
+    x = randn(1, 1, n, d)
+    pos = torch.randint(2 ** 30, 2 ** 31, (1, n), generator=g).int()
+    f = -torch.rand(32, generator=g) * 10.0 ** torch.randint(-5, 0, (32,), generator=g).float()
+    for adjacent in (False, True):
+        for p in (pos, -pos):
+            out = lb.lsh_rope(x.cuda(), p.cuda(), f.cuda(), axis_dims=(64,), adjacent=adjacent)
+            size = x.double().abs()
+            size = size + (size.unflatten(-1, (-1, 2)).flip(-1).flatten(-2) if adjacent else size.roll(32, -1))
+            near(out, oc.rope(x, p, f, (64,), adjacent), size * 2.0 ** -22, "out")
