@@ -270,3 +270,15 @@ def test_rope_negative_frequencies_at_far_positions():
             size = x.double().abs()
             size = size + (size.unflatten(-1, (-1, 2)).flip(-1).flatten(-2) if adjacent else size.roll(32, -1))
             near(out, oc.rope(x, p, f, (64,), adjacent), size * 2.0 ** -22, "out")
+
+
+def test_rope_does_not_write_heads_over_one_another():
+    x = randn(2, 5, 3, 64).bfloat16().cuda()
+    pos, f = torch.arange(3, dtype=torch.int32, device=DEV)[None], freqs_of((64,)).cuda()
+    base = torch.zeros_like(x)
+    with pytest.raises(lb.LshAttnError):
+        lb.lsh_rope(x, pos, f, axis_dims=(64,), out=base[:, :1].expand(-1, 5, -1, -1))
+    with pytest.raises(lb.LshAttnError):
+        lb.lsh_rope(x, pos, f, axis_dims=(64,), out=base[:1].expand(2, -1, -1, -1))
+    torch.cuda.synchronize()
+    assert (base == 0).all()
