@@ -182,9 +182,10 @@ __device__ __forceinline__ float inv_norm(const float (&f)[8], bool in) {
 // order); this block alone owns the page's head, so earlier rows are rounded again
 // in place. A stream of rows in and out, bound by DRAM in bf16: 64
 // us for 4 x 8192 rows of 8 heads of 128 with a rotation (0.80 of the copy rate; 48 us
-// without one, which writes a third less). int8 is bound by its instructions (two
-// thirds of the issue slots, with DRAM mostly idle): 94 us there (0.43); with every
-// thread forming the scales itself, two barriers of a head's four left out, 96.
+// without one, which writes a third less). int8 is near none of
+// its limits: two thirds of the issue slots, 41% of the warps active, waits at its four
+// barriers a head among the first stalls, DRAM mostly idle: 95 us there (0.43); with every
+// thread forming the scales itself, two of the barriers left out, 96.
 // grid (blocks of rows, head groups, batch), block append_threads(D, R).
 template <int D, bool I8, int R, int TURN>
 __global__ void __launch_bounds__(append_threads(D, R), 1024 / append_threads(D, R))

@@ -101,9 +101,11 @@ lsh_status launch_rope(RopeArgs A, const void* x, void* out, cudaStream_t st) {
     else if (w == 4) kern = k_rope<T, D, 4, false>;
     else if (w == 2) kern = k_rope<T, D, 2, false>;
   }
-  // Neighbouring pairs: a job a block (0.91 of the copy rate at B1 H8 n65536 d128;
+  // Neighbouring pairs: a job a block (0.89 of the copy rate at B1 H8 n65536 d128;
   // persistent blocks 0.84). Halves have more to work out before the first row:
   // persistent blocks (0.75 at B8 H8 n12288 d64, axes 24, 24, 16; a job a block 0.61).
+  // (Measured with runs of four. Narrower ones have registers for two or three blocks an
+  // SM only and take the same grid: 0.57 at axes 10, 14.)
   const int64_t jobs = tiles * A.head_groups;
   const int64_t most = A.rot.adjacent ? INT32_MAX : 5 * sm_count();
   const int64_t blocks = std::min(jobs, most), rest = blocks / A.tiles;

@@ -188,10 +188,12 @@ struct RopeArgs {
 // kernel besides DRAM is the instructions beside the rotation itself: where a
 // piece lies, the phases, the angles. Rows come by cp.async, two batches of heads
 // ahead, and are under way meanwhile. Halves: the lanes of a row form each angle
-// once and find their partners' pieces in shared memory. Measured: 45 us at B1 H8
-// n65536 d128, neighbours (0.91 of the copy rate), 41 us at B8 H8 n12288 d64, axes
+// once and find their partners' pieces in shared memory. Measured: 45.8 us at B1 H8
+// n65536 d128, neighbours (0.89 of the copy rate), 41 us at B8 H8 n12288 d64, axes
 // 24, 24, 16 by halves (0.75; with partners read from global memory too, 95 us; a
-// position fetched for each angle when it is formed, 43 us).
+// position fetched for each angle when it is formed, 43 us). Halves in runs of one or
+// two take 76 to 115 registers: two or three blocks an SM (axes 44, 42, 42 at the first of
+// these sizes 61.6 us, 0.67; axes 10, 14 at the second 53.9, 0.57).
 // grid (blocks), block 256.
 template <typename T, int D, int W, bool ADJ>
 __global__ void __launch_bounds__(256, ADJ || W < 4 ? 0 : 5) k_rope(const T* x, T* out, RopeArgs A) {
